@@ -48,7 +48,7 @@
  *     otherwise DSA_ERR_MISALIGNED.
  *   - Supported shapes: (h_idx, d_idx) in {(64,128), (4,32)}; (h, d_qk, d_v) in
  *     {(128,576,512), (16,160,128)}; topk a multiple of 64 in [64, 2048]; block_size 64.
- *     Decode needs (h_idx, d_idx) = (64,128).  Anything else: DSA_ERR_UNSUPPORTED_SHAPE.
+ *     DECODE needs (h_idx, d_idx) = (64,128).  Anything else: DSA_ERR_UNSUPPORTED_SHAPE.
  *
  * Geometry (dsa_seqs_t):
  *   PREFILL: total_rows packed query rows; row r of sequence b (cu[b] <= r < cu[b+1]) has
@@ -58,6 +58,14 @@
  *            it sees keys 0..seq_lens[b]-1.  Logical key s of sequence b is physical row
  *            block_table[b, s / block_size] * block_size + s % block_size, or, with
  *            block_table == NULL, b * max_seqlen + s.
+ *   CHUNK  : several new tokens per sequence over the same (paged) caches as DECODE: a chunk of a
+ *            prompt, drafted tokens to verify, or a mix with single tokens.  total_rows packed
+ *            query rows; sequence b's new tokens are rows cu[b] <= r < cu[b+1] (possibly none)
+ *            and the last of its seq_lens[b] cached tokens: row r has position pos =
+ *            seq_lens[b] - (cu[b+1] - r) and sees keys 0..pos.  Keys lie where DECODE has them.
+ *            A context above max_seqlen is taken as max_seqlen, and a row whose position comes
+ *            out negative has no keys; both set DSA_DEVICE_BAD_INDEX.  The training calls take
+ *            no chunks (DSA_ERR_INVALID_ARG).
  *   Key indices returned by dsa_topk and consumed by dsa_sparse_mla_fwd are LOGICAL
  *   positions within the sequence.
  */
@@ -96,7 +104,7 @@ typedef enum {
 #define DSA_DEVICE_TIMEOUT 1
 #define DSA_DEVICE_BAD_INDEX 2
 
-enum { DSA_PREFILL = 0, DSA_DECODE = 1 };
+enum { DSA_PREFILL = 0, DSA_DECODE = 1, DSA_CHUNK = 2 };
 
 typedef struct {
   int32_t h_idx;        /* indexer heads */
@@ -110,16 +118,17 @@ typedef struct {
 } dsa_dims_t;
 
 typedef struct {
-  int32_t mode;                  /* DSA_PREFILL or DSA_DECODE */
+  int32_t mode;                  /* DSA_PREFILL, DSA_DECODE or DSA_CHUNK */
   int32_t batch;                 /* sequences */
-  int32_t total_rows;            /* query rows: prefill cu_seqlens[batch]; decode batch */
-  int32_t max_seqlen;            /* longest sequence; decode without block table: row stride */
+  int32_t total_rows;            /* query rows: prefill, chunk cu_seqlens[batch]; decode batch */
+  int32_t max_seqlen;            /* longest sequence (chunk: longest context); decode and chunk
+                                    without block table: row stride */
   int64_t num_kv_rows;           /* physical rows of k_idx, k_scale and kv */
-  const int32_t* cu_seqlens;     /* PREFILL: device [batch+1], cu[0] = 0, non-decreasing */
-  const int32_t* cu_seqlens_host;/* PREFILL: host copy of cu_seqlens, used for planning */
-  const int32_t* seq_lens;       /* DECODE : device [batch], each in [1, max_seqlen] */
-  const int32_t* block_table;    /* DECODE : device [batch, max_blocks] or NULL */
-  int32_t max_blocks;            /* DECODE : columns of block_table */
+  const int32_t* cu_seqlens;     /* PREFILL, CHUNK: device [batch+1], cu[0] = 0, non-decreasing */
+  const int32_t* cu_seqlens_host;/* PREFILL, CHUNK: host copy of cu_seqlens, for planning */
+  const int32_t* seq_lens;       /* DECODE, CHUNK: device [batch], each in [1, max_seqlen] */
+  const int32_t* block_table;    /* DECODE, CHUNK: device [batch, max_blocks] or NULL */
+  int32_t max_blocks;            /* DECODE, CHUNK: columns of block_table */
 } dsa_seqs_t;
 
 /* Stage 1.  Scores of query rows [row_begin, row_begin + row_count) against their prior
@@ -201,8 +210,9 @@ DSA_API size_t dsa_sparse_mla_workspace_size_for(const dsa_dims_t* dims, const d
  *   idx  int32 [row_count, topk] logical key indices (-1 = unused), relative to row_begin,
  *        or NULL: every prior key of each row (dense causal attention), which is exactly the
  *        top-k's selection when no row has more than topk prior keys, and the dense model's
- *        attention (the training's warm-up stage) when rows are longer.  PREFILL rows of any
- *        length; DECODE with NULL needs max_seqlen <= topk (else DSA_ERR_INVALID_ARG)
+ *        attention (the training's warm-up stage) when rows are longer.  PREFILL and CHUNK rows
+ *        of any length (CHUNK: max_seqlen up to 131072, else DSA_ERR_UNSUPPORTED_SHAPE); DECODE
+ *        with NULL needs max_seqlen <= topk (else DSA_ERR_INVALID_ARG)
  *   out  bf16 [total_rows, h, d_v] and lse fp32 [total_rows, h] (absolute rows); a row
  *        with no valid index gets out = 0 and lse = -inf. */
 DSA_API dsa_status_t dsa_sparse_mla_fwd(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
@@ -293,8 +303,9 @@ DSA_API dsa_status_t dsa_forward_rows(const dsa_dims_t* dims, const dsa_seqs_t* 
 
 /* Decode cache append, the step that fills the caches the path reads ("FP8 index -> top-k
  * selection -> sparse core attention", "DeepSeek V3.2-Exp Cuts Long-Context Costs with DeepSeek
- * Sparse Attention (DSA)", pipeline summary: the indexer reads keys in FP8).  DECODE mode only.
- * For each sequence b the new token sits at position p = seq_lens[b] - 1 (the lengths already
+ * Sparse Attention (DSA)", pipeline summary: the indexer reads keys in FP8).  DECODE or CHUNK
+ * mode (CHUNK: total_rows new tokens, row r at its own position, skipped and reported when its
+ * context is above max_seqlen).  For each sequence b of a DECODE call the new token sits at position p = seq_lens[b] - 1 (the lengths already
  * count it); it is written at physical row block_table[b][p / block_size] * block_size +
  * p % block_size, or b * max_seqlen + p when block_table is NULL:
  *   k_new     fp32 [batch, d_idx]: the new token's indexer key, quantised per token: scale =
@@ -309,6 +320,75 @@ DSA_API dsa_status_t dsa_cache_append(const dsa_dims_t* dims, const dsa_seqs_t* 
                                       const float* k_new, const uint16_t* kv_new,
                                       uint8_t* k_cache, float* k_scale_cache, uint16_t* kv_cache,
                                       int32_t* dev_status, dsa_stream_t stream);
+
+/* ---- 8-bit latent cache -------------------------------------------------------------------
+ * The latent rows of the caches in 8 bits: 0.57 of the bf16 row's bytes, so that a GPU holds
+ * 1.75 times the context and a step reads that much less of it.  Row of one token,
+ * dsa_q8_row_bytes(dims) bytes (656 at d_qk 576, d_v 512; 208 at 160, 128):
+ *   d_v        e4m3 codes of the d_v latent values
+ *   16 n       fp32 scales, one per 128 values, padded with zeros to a multiple of 16 bytes
+ *   2 (d_qk - d_v)   the rotary dims in bf16, unquantised
+ * A scale is the smallest power of two s with max|x| <= 448 s over its 128 values (1 when all are
+ * 0; its exponent kept within [-100, 119]), a code the e4m3 value nearest to x / s (ties to even,
+ * saturating), so that |x - s code| <= 2^-4 |x| + 2^-10 s.  s code is exact in bf16: reading back
+ * and attending round nothing more.  128 values that hold an infinity or a NaN get a NaN scale
+ * and read back as NaN.  Row number r of the cache starts at byte r * dsa_q8_row_bytes; rows,
+ * pages and block tables are those of the bf16 cache. */
+
+/* Bytes of one 8-bit latent row; 0 when (d_qk, d_v) is not a supported pair. */
+DSA_API size_t dsa_q8_row_bytes(const dsa_dims_t* dims);
+
+/* dsa_cache_append into an 8-bit latent cache: the new tokens' indexer keys are quantised and
+ * written as there, their latent rows quantised into kv8_cache [num_kv_rows] rows.  DECODE (one
+ * token per sequence) or CHUNK (total_rows tokens); k_new [total_rows, d_idx], kv_new
+ * [total_rows, d_qk].  Tokens without a place in the caches are skipped, every other row is left
+ * as it was. */
+DSA_API dsa_status_t dsa_cache_append_q8(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
+                                         const float* k_new, const uint16_t* kv_new,
+                                         uint8_t* k_cache, float* k_scale_cache,
+                                         uint8_t* kv8_cache, int32_t* dev_status,
+                                         dsa_stream_t stream);
+
+/* Reads ranges of the 8-bit cache back as packed bf16 latent rows (exact: see above), e.g. the
+ * prefix a dense pass or another cache wants.  DECODE or CHUNK geometry (seq_lens and the block
+ * table are used, not the query rows).
+ *   cu_keys    device int32 [batch + 1], cu_keys[0] = 0, non-decreasing: range b is output rows
+ *              cu_keys[b] .. cu_keys[b+1] - 1
+ *   key_begin  device int32 [batch], first logical key of each range, or NULL: 0
+ *   total_keys cu_keys[batch] (the host's copy; with a smaller one the rows past it are not
+ *              written, and rows from cu_keys[batch] on never are)
+ *   kv_out     bf16 [total_keys, d_qk]
+ * A key outside its sequence's context or the caches reads as zeros and sets
+ * DSA_DEVICE_BAD_INDEX.  All pointers 16-byte aligned. */
+DSA_API dsa_status_t dsa_cache_read_q8(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
+                                       const uint8_t* kv8_cache, const int32_t* key_begin,
+                                       const int32_t* cu_keys, int32_t total_keys,
+                                       uint16_t* kv_out, int32_t* dev_status,
+                                       dsa_stream_t stream);
+
+/* dsa_sparse_mla_fwd over the 8-bit cache, DECODE or CHUNK, with a workspace of
+ * dsa_sparse_mla_q8_workspace_size bytes.  idx NULL: every prior key, max_seqlen up to 131072
+ * (else DSA_ERR_UNSUPPORTED_SHAPE).  Logits, softmax and LSE are those of the values read back;
+ * sums are fp32, the probabilities are rounded to bf16 for the product with the values. */
+DSA_API size_t dsa_sparse_mla_q8_workspace_size(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
+                                                int32_t row_count);
+DSA_API dsa_status_t dsa_sparse_mla_fwd_q8(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
+                                           const uint16_t* q, const uint8_t* kv8,
+                                           const int32_t* idx, int32_t row_begin,
+                                           int32_t row_count, uint16_t* out, float* lse,
+                                           void* workspace, size_t workspace_bytes,
+                                           int32_t* dev_status, dsa_stream_t stream);
+
+/* dsa_forward over the 8-bit latent cache, DECODE or CHUNK (the indexer's caches are the same),
+ * with a workspace of dsa_forward_q8_workspace_size bytes. */
+DSA_API size_t dsa_forward_q8_workspace_size(const dsa_dims_t* dims, const dsa_seqs_t* seqs);
+DSA_API dsa_status_t dsa_forward_q8(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
+                                    const uint8_t* q_idx, const float* q_scale, const float* w,
+                                    const uint8_t* k_idx, const float* k_scale, const uint16_t* q,
+                                    const uint8_t* kv8, int32_t* idx_out, float* sel_out,
+                                    uint16_t* out, float* lse, void* workspace,
+                                    size_t workspace_bytes, int32_t* dev_status,
+                                    dsa_stream_t stream);
 
 /* ---- indexer training (sparse stage) ------------------------------------------------------
  * The indexer is trained to imitate the main attention's head-summed distribution through a KL

@@ -36,6 +36,7 @@ DSA_DEVICE_BAD_INDEX = 2
 TOPK_HIST_BINS = 2048
 DSA_PREFILL = 0
 DSA_DECODE = 1
+DSA_CHUNK = 2
 
 EXPORTED = ("dsa_indexer_scores", "dsa_topk", "dsa_sparse_mla_workspace_size",
             "dsa_sparse_mla_fwd", "dsa_forward_workspace_size", "dsa_forward",
@@ -45,7 +46,9 @@ EXPORTED = ("dsa_indexer_scores", "dsa_topk", "dsa_sparse_mla_workspace_size",
             "dsa_sparse_mla_workspace_size_for", "dsa_indexer_topk",
             "dsa_indexer_topk_workspace_size", "dsa_forward_chunk_rows_for",
             "dsa_forward_rows", "dsa_indexer_kl_target_dense", "dsa_indexer_kl_backward_dense",
-            "dsa_probe_dsmem", "dsa_probe_page_stream")
+            "dsa_probe_dsmem", "dsa_probe_page_stream", "dsa_q8_row_bytes", "dsa_cache_append_q8",
+            "dsa_cache_read_q8", "dsa_sparse_mla_q8_workspace_size", "dsa_sparse_mla_fwd_q8",
+            "dsa_forward_q8_workspace_size", "dsa_forward_q8")
 NOALLOC_SCRATCH_BYTES = 20 << 20
 
 
@@ -106,6 +109,13 @@ def _load():
         "dsa_abi_version": (I32, []),
         "dsa_sparse_mla_fwd_noalloc": (I32, [DP, SP, P, P, P, I32, I32, P, P, P, P]),
         "dsa_cache_append": (I32, [DP, SP, P, P, P, P, P, P, P]),
+        "dsa_q8_row_bytes": (SZ, [DP]),
+        "dsa_cache_append_q8": (I32, [DP, SP, P, P, P, P, P, P, P]),
+        "dsa_cache_read_q8": (I32, [DP, SP, P, P, P, I32, P, P, P]),
+        "dsa_sparse_mla_q8_workspace_size": (SZ, [DP, SP, I32]),
+        "dsa_sparse_mla_fwd_q8": (I32, [DP, SP, P, P, P, I32, I32, P, P, P, SZ, P, P]),
+        "dsa_forward_q8_workspace_size": (SZ, [DP, SP]),
+        "dsa_forward_q8": (I32, [DP, SP, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -157,16 +167,21 @@ def make_problem(*, mode: str, h_idx: int, d_idx: int, h: int, d_qk: int, d_v: i
                  seq_lens=None, block_table=None, max_seqlen: Optional[int] = None,
                  block_size: int = 64) -> Problem:
     """Builds dsa_dims_t / dsa_seqs_t.  ``cu_seqlens``, ``seq_lens``, ``block_table`` are device
-    int32 tensors; ``seqlens`` is the host list of sequence lengths."""
+    int32 tensors; ``seqlens`` is the host list of sequence lengths, for mode "chunk" of new
+    tokens per sequence (``max_seqlen``, the longest context, is then required)."""
     dims = dsa_dims_t(h_idx, d_idx, h, d_qk, d_v, topk, block_size, softmax_scale)
     seqlens = [int(x) for x in seqlens]
+    if mode == "chunk" and not max_seqlen:
+        raise ValueError("a chunk problem needs max_seqlen, its longest context")
     max_len = int(max_seqlen or max(seqlens))
     keep = []
     s = dsa_seqs_t()
     s.batch = len(seqlens)
     s.max_seqlen = max_len
     s.num_kv_rows = int(num_kv_rows)
-    if mode == "prefill":
+    if mode not in ("prefill", "decode", "chunk"):
+        raise ValueError(f"mode {mode!r}: prefill, decode or chunk")
+    if mode != "decode":
         host = (ctypes.c_int32 * (len(seqlens) + 1))()
         acc = 0
         for i, L in enumerate(seqlens):
@@ -174,13 +189,14 @@ def make_problem(*, mode: str, h_idx: int, d_idx: int, h: int, d_qk: int, d_v: i
             acc += L
         host[len(seqlens)] = acc
         keep.append(host)
-        s.mode = DSA_PREFILL
+        s.mode = DSA_PREFILL if mode == "prefill" else DSA_CHUNK
         s.total_rows = acc
         s.cu_seqlens = _ptr(cu_seqlens)
         s.cu_seqlens_host = ctypes.cast(host, ctypes.c_void_p)
     else:
         s.mode = DSA_DECODE
         s.total_rows = len(seqlens)
+    if mode != "prefill":
         s.seq_lens = _ptr(seq_lens)
         s.block_table = _ptr(block_table)
         s.max_blocks = int(block_table.shape[1]) if block_table is not None else 0
@@ -301,6 +317,53 @@ def dsa_cache_append(pb: Problem, k_new, kv_new, k_cache, k_scale_cache, kv_cach
     return int(lib.dsa_cache_append(
         ctypes.byref(pb.dims), ctypes.byref(pb.seqs), _ptr(k_new), _ptr(kv_new), _ptr(k_cache),
         _ptr(k_scale_cache), _ptr(kv_cache), _ptr(dev_status), _stream(stream)))
+
+
+def dsa_q8_row_bytes(pb: Problem) -> int:
+    return int(lib.dsa_q8_row_bytes(ctypes.byref(pb.dims)))
+
+
+def dsa_cache_append_q8(pb: Problem, k_new, kv_new, k_cache, k_scale_cache, kv8_cache,
+                        dev_status=None, stream=None) -> int:
+    return int(lib.dsa_cache_append_q8(
+        ctypes.byref(pb.dims), ctypes.byref(pb.seqs), _ptr(k_new), _ptr(kv_new), _ptr(k_cache),
+        _ptr(k_scale_cache), _ptr(kv8_cache), _ptr(dev_status), _stream(stream)))
+
+
+def dsa_cache_read_q8(pb: Problem, kv8_cache, key_begin, cu_keys, total_keys: int, kv_out,
+                      dev_status=None, stream=None) -> int:
+    """key_begin: device int32 [batch] or None (each range starts at key 0); cu_keys: device int32
+    [batch + 1], the packed output rows of each sequence's range."""
+    return int(lib.dsa_cache_read_q8(
+        ctypes.byref(pb.dims), ctypes.byref(pb.seqs), _ptr(kv8_cache), _ptr(key_begin),
+        _ptr(cu_keys), total_keys, _ptr(kv_out), _ptr(dev_status), _stream(stream)))
+
+
+def dsa_sparse_mla_q8_workspace_size(pb: Problem, row_count: int) -> int:
+    return int(lib.dsa_sparse_mla_q8_workspace_size(ctypes.byref(pb.dims), ctypes.byref(pb.seqs),
+                                                    row_count))
+
+
+def dsa_sparse_mla_fwd_q8(pb: Problem, q, kv8, idx, row_begin: int, row_count: int, out, lse,
+                          workspace=None, workspace_bytes: int = 0, dev_status=None,
+                          stream=None) -> int:
+    return int(lib.dsa_sparse_mla_fwd_q8(
+        ctypes.byref(pb.dims), ctypes.byref(pb.seqs), _ptr(q), _ptr(kv8), _ptr(idx), row_begin,
+        row_count, _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes, _ptr(dev_status),
+        _stream(stream)))
+
+
+def dsa_forward_q8_workspace_size(pb: Problem) -> int:
+    return int(lib.dsa_forward_q8_workspace_size(ctypes.byref(pb.dims), ctypes.byref(pb.seqs)))
+
+
+def dsa_forward_q8(pb: Problem, q_idx, q_scale, w, k_idx, k_scale, q, kv8, idx_out, out, lse,
+                   workspace, workspace_bytes: int, dev_status=None, stream=None,
+                   sel_out=None) -> int:
+    return int(lib.dsa_forward_q8(
+        ctypes.byref(pb.dims), ctypes.byref(pb.seqs), _ptr(q_idx), _ptr(q_scale), _ptr(w),
+        _ptr(k_idx), _ptr(k_scale), _ptr(q), _ptr(kv8), _ptr(idx_out), _ptr(sel_out), _ptr(out),
+        _ptr(lse), _ptr(workspace), workspace_bytes, _ptr(dev_status), _stream(stream)))
 
 
 def dsa_indexer_kl_target(pb: Problem, q, kv, idx, lse, row_begin: int, row_count: int, target,

@@ -13,9 +13,11 @@
 
 #include "dsa.h"
 #include "cache_append.cuh"
+#include "cache_q8.cuh"
 #include "indexer.cuh"
 #include "indexer_bwd.cuh"
 #include "indexer_bwd_tc.cuh"
+#include "paged_mla.cuh"
 #include "sparse_mla.cuh"
 #include "topk.cuh"
 
@@ -140,7 +142,7 @@ dsa_status_t launch_status() {
 
 bool indexer_shape_ok(const dsa_dims_t& d, int mode) {
   if (d.h_idx == 64 && d.d_idx == 128) return true;
-  return mode == DSA_PREFILL && d.h_idx == 4 && d.d_idx == 32;
+  return mode != DSA_DECODE && d.h_idx == 4 && d.d_idx == 32;
 }
 
 bool mla_shape_ok(const dsa_dims_t& d) {
@@ -151,12 +153,13 @@ bool mla_shape_ok(const dsa_dims_t& d) {
 dsa_status_t check_common(const dsa_dims_t* dims, const dsa_seqs_t* seqs) {
   if (dims == nullptr || seqs == nullptr) return DSA_ERR_INVALID_ARG;
   const dsa_seqs_t& s = *seqs;
-  if (s.mode != DSA_PREFILL && s.mode != DSA_DECODE) return DSA_ERR_INVALID_ARG;
+  if (s.mode != DSA_PREFILL && s.mode != DSA_DECODE && s.mode != DSA_CHUNK)
+    return DSA_ERR_INVALID_ARG;
   if (s.batch <= 0 || s.total_rows < 0 || s.max_seqlen <= 0 || s.num_kv_rows <= 0)
     return DSA_ERR_INVALID_ARG;
   if (dims->topk < 64 || dims->topk > 2048 || dims->topk % 64 != 0)
     return DSA_ERR_UNSUPPORTED_SHAPE;
-  if (s.mode == DSA_PREFILL) {
+  if (s.mode != DSA_DECODE) {
     if (s.cu_seqlens == nullptr || s.cu_seqlens_host == nullptr) return DSA_ERR_INVALID_ARG;
     const int32_t* cu = s.cu_seqlens_host;
     if (cu[0] != 0 || cu[s.batch] != s.total_rows) return DSA_ERR_INVALID_ARG;
@@ -164,9 +167,11 @@ dsa_status_t check_common(const dsa_dims_t* dims, const dsa_seqs_t* seqs) {
       const int L = cu[b + 1] - cu[b];
       if (L < 0 || L > s.max_seqlen) return DSA_ERR_INVALID_ARG;
     }
-    if (s.total_rows > s.num_kv_rows) return DSA_ERR_INVALID_ARG;
-  } else {
-    if (s.seq_lens == nullptr || s.total_rows != s.batch) return DSA_ERR_INVALID_ARG;
+    if (s.mode == DSA_PREFILL && s.total_rows > s.num_kv_rows) return DSA_ERR_INVALID_ARG;
+  }
+  if (s.mode != DSA_PREFILL) {
+    if (s.seq_lens == nullptr || (s.mode == DSA_DECODE && s.total_rows != s.batch))
+      return DSA_ERR_INVALID_ARG;
     if (dims->block_size != 64) return DSA_ERR_UNSUPPORTED_SHAPE;
     if (s.block_table != nullptr) {
       if (s.max_blocks < ceil_div(s.max_seqlen, 64)) return DSA_ERR_INVALID_ARG;
@@ -185,7 +190,7 @@ dsa_status_t check_rows(const dsa_seqs_t* s, int32_t row_begin, int32_t row_coun
 
 // Largest key count (pos + 1) among rows [row_begin, row_begin + row_count).
 int64_t max_keys(const dsa_seqs_t* s, int32_t row_begin, int32_t row_count) {
-  if (s->mode == DSA_DECODE) return s->max_seqlen;
+  if (s->mode != DSA_PREFILL) return s->max_seqlen;
   const int32_t* cu = s->cu_seqlens_host;
   int64_t m = 0;
   for (int b = 0; b < s->batch; ++b) {
@@ -199,9 +204,9 @@ int64_t max_keys(const dsa_seqs_t* s, int32_t row_begin, int32_t row_count) {
 // Without an index array attention runs dense: every prior key of each row (the top-k's
 // selection when no row has more than topk prior keys; dense causal attention in general).
 // Decode rows take at most topk keys that way (resolved through the block table up front);
-// prefill rows of any length (their keys are consecutive packed rows, streamed past topk).
+// prefill and chunk rows of any length (streamed past topk; a chunk's tiles are whole pages).
 bool dense_ok(const dsa_dims_t& d, const dsa_seqs_t* s, int32_t row_begin, int32_t row_count) {
-  return s->mode == DSA_PREFILL || max_keys(s, row_begin, row_count) <= d.topk;
+  return s->mode != DSA_DECODE || max_keys(s, row_begin, row_count) <= d.topk;
 }
 
 // The training target without indices writes topk entries per row: rows of at most topk keys.
@@ -248,9 +253,9 @@ dsa_status_t make_block_map(CUtensorMap* map, const void* base, uint64_t blocks,
   return r == CUDA_SUCCESS ? DSA_OK : DSA_ERR_CUDA;
 }
 
-// The indexer's scales may live inside the key blocks (k_scale NULL) only in paged decode.
+// The indexer's scales may live inside the key blocks (k_scale NULL) only in paged caches.
 bool interleaved_ok(const dsa_seqs_t& s) {
-  return s.mode == DSA_DECODE && s.block_table != nullptr && s.num_kv_rows % 64 == 0;
+  return s.mode != DSA_PREFILL && s.block_table != nullptr && s.num_kv_rows % 64 == 0;
 }
 
 // Rows of `row_bytes` bytes (a multiple of 16), boxes of box_bytes x box_rows, 128-byte swizzle.
@@ -271,13 +276,13 @@ dsa_status_t make_row_map(CUtensorMap* map, const void* base, uint64_t rows, uin
 
 // ------------------------------------------------------------------------ stage 1
 
-template <int H_I, int D_I, int QPG>
+template <int H_I, int D_I, int QPG, bool kChunk = false>
 dsa_status_t run_indexer_kernel(const CUtensorMap& kmap, const CUtensorMap& qmap,
                                 const IndexerParams& prm, dim3 grid, cudaStream_t st) {
-  using C = IndexerCfg<H_I, D_I, QPG>;
+  using C = IndexerCfg<H_I, D_I, QPG, kChunk>;
   int smem = C::SMEM_BYTES;
   if (C::TMEM_COLS == 512) smem = std::max(smem, 120 * 1024);   // one CTA per SM
-  auto k = dsa_indexer_kernel<H_I, D_I, QPG>;
+  auto k = dsa_indexer_kernel<H_I, D_I, QPG, kChunk>;
   if (prepare_kernel(k, smem) != DSA_OK) return DSA_ERR_CUDA;
   // may launch while the previous kernel finishes (the kernel waits for it before any read)
   return launch_pdl(k, grid, C::THREADS, smem, st, kmap, qmap, prm);
@@ -319,12 +324,13 @@ dsa_status_t indexer_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint8_
   if (k_scale == nullptr) {
     if (make_block_map(&kmap, k_idx, uint64_t(s.num_kv_rows / 64), D_I) != DSA_OK)
       return DSA_ERR_CUDA;
-  } else if (make_map(&kmap, k_idx, s.num_kv_rows, D_I, s.mode == DSA_DECODE ? 64 : 128) !=
+  } else if (make_map(&kmap, k_idx, s.num_kv_rows, D_I, s.mode != DSA_PREFILL ? 64 : 128) !=
              DSA_OK) {
     return DSA_ERR_CUDA;
   }
-  if (make_map(&qmap, q_idx, uint64_t(s.total_rows) * H_I, D_I, C::N) != DSA_OK)
-    return DSA_ERR_CUDA;
+  // (a chunk's map ends with the row range: a partial last group reads zeros past it)
+  const uint64_t q_rows = s.mode == DSA_CHUNK ? uint64_t(row_begin) + row_count : s.total_rows;
+  if (make_map(&qmap, q_idx, q_rows * H_I, D_I, C::N) != DSA_OK) return DSA_ERR_CUDA;
   IndexerParams prm{};
   prm.q_scale = q_scale;
   prm.w = w;
@@ -353,8 +359,30 @@ dsa_status_t indexer_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint8_
     prm.tiles_per_split = static_cast<int32_t>(tps);
     return run_indexer_kernel<H_I, D_I, QPG>(kmap, qmap, prm, dim3(row_count, splits), st);
   }
-  // prefill: one launch per sequence segment of the row range
   const int32_t* cu = s.cu_seqlens_host;
+  if constexpr (QPG > 1) {
+    if (s.mode == DSA_CHUNK) {
+      // one launch over the query groups of every sequence (each CTA finds its own)
+      int64_t groups = 0;
+      for (int b = 0; b < s.batch; ++b) {
+        const int64_t lo = std::max<int64_t>(cu[b], row_begin);
+        const int64_t hi = std::min<int64_t>(cu[b + 1], int64_t(row_begin) + row_count);
+        if (lo < hi) groups += ceil_div(hi - lo, QPG);
+      }
+      const int64_t tiles = ceil_div(s.max_seqlen, 128);
+      int64_t splits = std::min<int64_t>(tiles, std::max<int64_t>(1, ceil_div(target, groups)));
+      const int64_t tps = std::max<int64_t>(ceil_div(tiles, splits), std::min<int64_t>(tiles, 8));
+      splits = ceil_div(tiles, tps);
+      prm.row0 = row_begin;
+      prm.nrows = row_count;
+      prm.out_row0 = 0;
+      prm.cu_seqlens = s.cu_seqlens;
+      prm.batch = s.batch;
+      prm.tiles_per_split = static_cast<int32_t>(tps);
+      return run_indexer_kernel<H_I, D_I, QPG, true>(kmap, qmap, prm, dim3(groups, splits), st);
+    }
+  }
+  // prefill: one launch per sequence segment of the row range
   for (int b = 0; b < s.batch; ++b) {
     const int64_t lo = std::max<int64_t>(cu[b], row_begin);
     const int64_t hi = std::min<int64_t>(cu[b + 1], int64_t(row_begin) + row_count);
@@ -453,6 +481,7 @@ dsa_status_t topk_launch(const dsa_dims_t& d, const dsa_seqs_t& s, const float* 
   prm.sel = sel;
   prm.topk = d.topk;
   prm.decode = s.mode == DSA_DECODE;
+  prm.chunk = s.mode == DSA_CHUNK;
   prm.row_begin = row_begin;
   prm.batch = s.batch;
   prm.cu_seqlens = s.cu_seqlens;
@@ -493,10 +522,31 @@ size_t mla_ws_bytes(const dsa_dims_t& d, int splits, int32_t row_count) {
   return size_t(splits) * row_count * d.h * (d.d_v + 1) * sizeof(float) + 256;
 }
 
+// Split-KV slices per row of the paged attention, chosen as mla_splits below chooses them.
+int paged_splits(const dsa_dims_t& d, const dsa_seqs_t& s, int32_t row_count, int sm_count,
+                 size_t max_ws = SIZE_MAX) {
+  if (s.mode == DSA_PREFILL || row_count <= 0) return 1;
+  const int tiles = std::max(1, (std::min(d.topk, std::max(1, s.max_seqlen)) + 63) / 64);
+  const int sms = std::max(1, sm_count);
+  int best = 1;
+  double best_t = 1e30;
+  for (int sp = 1; sp <= std::min(16, std::max(1, tiles / 4)); ++sp) {
+    if (mla_ws_bytes(d, sp, row_count) > max_ws) continue;
+    const double waves = std::ceil(2.0 * row_count * sp / sms);
+    const double t = waves * (3.0 + std::ceil(double(tiles) / sp)) + (sp > 1 ? 2.0 : 0.0);
+    if (t < best_t - 1e-9) {
+      best_t = t;
+      best = sp;
+    }
+  }
+  return best;
+}
+
 // Split-KV slices per decode row.  Only speed depends on the choice: one split needs no
 // partials, so a cap on the partials' bytes (max_ws) always leaves a valid answer.
 int mla_splits(const dsa_dims_t& d, const dsa_seqs_t& s, int32_t row_count, int sm_count,
                size_t max_ws = SIZE_MAX) {
+  if (s.mode == DSA_CHUNK) return paged_splits(d, s, row_count, sm_count, max_ws);
   if (s.mode != DSA_DECODE || row_count <= 0) return 1;
   // Two CTAs (one per value half) per row and split; one CTA per SM.  Pick the split count
   // with the smallest estimated makespan: waves x (prologue + tiles per split), in tile units
@@ -515,6 +565,12 @@ int mla_splits(const dsa_dims_t& d, const dsa_seqs_t& s, int32_t row_count, int 
     }
   }
   return best;
+}
+
+// Rows over the paged caches (decode and chunks) in the form the paged kernels take.
+PagedSeqs paged_seqs(const dsa_seqs_t& s) {
+  return PagedSeqs{s.mode == DSA_CHUNK, s.batch, s.cu_seqlens, s.seq_lens, s.block_table,
+                   s.max_blocks, s.max_seqlen, s.num_kv_rows};
 }
 
 // The inputs and row geometry shared by the attention forward and the target pass.
@@ -577,11 +633,74 @@ dsa_status_t mla_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint16_t* 
   return DSA_OK;
 }
 
+// Attention over the paged caches: chunks over bf16 rows, decode and chunks over 8-bit rows.
+template <int D_QK, int D_V, bool kQ8>
+dsa_status_t paged_mla_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint16_t* q,
+                            const void* kv, const int32_t* idx, int32_t row_begin,
+                            int32_t row_count, uint16_t* out, float* lse, void* ws,
+                            size_t ws_bytes, int32_t* status, cudaStream_t st, int splits) {
+  using C = MlaCfg<D_QK, D_V>;
+  PagedMlaParams prm{};
+  prm.s = paged_seqs(s);
+  prm.kv = static_cast<const uint8_t*>(kv);
+  prm.idx = idx;
+  prm.out = reinterpret_cast<__nv_bfloat16*>(out);
+  prm.lse = lse;
+  prm.row_begin = row_begin;
+  prm.row_count = row_count;
+  prm.topk = d.topk;
+  prm.h = d.h;
+  prm.splits = splits;
+  prm.scale_log2 = d.softmax_scale * 1.4426950408889634f;
+  prm.status = status;
+  // without indices a split's pages are resolved up front
+  if (idx == nullptr && ceil_div(ceil_div(s.max_seqlen, 64), splits) > kMaxDenseTiles)
+    return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (splits > 1) {
+    if (ws == nullptr || ws_bytes < mla_ws_bytes(d, splits, row_count))
+      return DSA_ERR_WORKSPACE_TOO_SMALL;
+    prm.part_o = static_cast<float*>(ws);
+    prm.part_lse = prm.part_o + size_t(splits) * row_count * d.h * D_V;
+  }
+  // Q in 64-dim x h-head boxes, no further than the row range
+  CUtensorMap q_map;
+  if (make_row_map(&q_map, q, (uint64_t(row_begin) + row_count) * d.h, D_QK * 2, 128, d.h) !=
+      DSA_OK)
+    return DSA_ERR_CUDA;
+  auto k = dsa_paged_mla_kernel<D_QK, D_V, kQ8>;
+  if (prepare_kernel(k, C::SMEM_BYTES) != DSA_OK) return DSA_ERR_CUDA;
+  if (launch_pdl(k, dim3(2 * row_count, splits), C::THREADS, C::SMEM_BYTES, st, q_map, prm) !=
+      DSA_OK)
+    return DSA_ERR_CUDA;
+  if (splits > 1) {
+    dsa_paged_combine_kernel<D_V><<<dim3(row_count, d.h), D_V / 4, 0, st>>>(prm);
+    return launch_status();
+  }
+  return DSA_OK;
+}
+
+dsa_status_t paged_mla_dispatch(const dsa_dims_t& d, const dsa_seqs_t& s, const uint16_t* q,
+                                const void* kv, bool q8, const int32_t* idx, int32_t row_begin,
+                                int32_t row_count, uint16_t* out, float* lse, void* ws,
+                                size_t ws_bytes, int32_t* status, cudaStream_t st, int splits) {
+  if (row_count == 0) return DSA_OK;
+  auto run = [&](auto impl) {
+    return impl(d, s, q, kv, idx, row_begin, row_count, out, lse, ws, ws_bytes, status, st,
+                splits);
+  };
+  if (d.d_qk == 576)
+    return q8 ? run(paged_mla_impl<576, 512, true>) : run(paged_mla_impl<576, 512, false>);
+  return q8 ? run(paged_mla_impl<160, 128, true>) : run(paged_mla_impl<160, 128, false>);
+}
+
 dsa_status_t mla_dispatch(const dsa_dims_t& d, const dsa_seqs_t& s, const uint16_t* q,
                           const uint16_t* kv, const int32_t* idx, int32_t row_begin,
                           int32_t row_count, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
                           int32_t* status, cudaStream_t st, int splits) {
   if (row_count == 0) return DSA_OK;
+  if (s.mode == DSA_CHUNK)
+    return paged_mla_dispatch(d, s, q, kv, false, idx, row_begin, row_count, out, lse, ws,
+                              ws_bytes, status, st, splits);
   if (d.d_qk == 576)
     return mla_impl<576, 512>(d, s, q, kv, idx, row_begin, row_count, out, lse, ws, ws_bytes,
                               status, st, splits);
@@ -597,6 +716,7 @@ struct ForwardPlan {
   int mla_splits = 1;
   size_t mla_bytes = 0;
   int64_t hist_rows = 0;     // first-digit histograms of one chunk's rows (fused indexer)
+  int64_t rows = 0;          // decode and chunks: rows per launch
   size_t total = 0;
 };
 
@@ -613,14 +733,37 @@ int64_t chunk_rows_for(int64_t L, int sm_count) {
   return cap >= wave ? cap / wave * wave : cap;
 }
 
-ForwardPlan plan_forward(const dsa_dims_t& d, const dsa_seqs_t& s, int sm_count) {
+// Rows per launch of a chunk problem: every row's scores may be max_seqlen long (the host does
+// not know the contexts), all rows in one launch when their slab fits the budget.
+int64_t paged_rows_for(const dsa_seqs_t& s, int sm_count) {
+  const int64_t cap = std::max<int64_t>(1, int64_t(kSlabBudget / (round4(s.max_seqlen) * 4)));
+  if (cap >= s.total_rows) return s.total_rows;
+  const int64_t wave = std::max(1, sm_count / 2);
+  return cap >= wave ? cap / wave * wave : cap;
+}
+
+// q8: the attention runs over the 8-bit cache (decode and chunks).
+ForwardPlan plan_forward(const dsa_dims_t& d, const dsa_seqs_t& s, int sm_count,
+                         bool q8 = false) {
   ForwardPlan p;
   if (s.mode == DSA_DECODE) {
     p.slab_floats = int64_t(s.batch) * round4(s.max_seqlen);
     p.idx_ints = int64_t(s.batch) * d.topk;
-    p.mla_splits = mla_splits(d, s, s.batch, sm_count);
+    p.mla_splits = q8 ? paged_splits(d, s, s.batch, sm_count)
+                      : mla_splits(d, s, s.batch, sm_count);
     p.mla_bytes = mla_ws_bytes(d, p.mla_splits, s.batch);
     p.hist_rows = s.batch;
+    p.rows = s.batch;
+  } else if (s.mode == DSA_CHUNK) {
+    p.rows = paged_rows_for(s, sm_count);
+    p.slab_floats = p.rows * round4(s.max_seqlen);
+    p.idx_ints = p.rows * d.topk;
+    p.hist_rows = p.rows;
+    // the last launch may have fewer rows and more splits
+    for (const int64_t rows : {p.rows, p.rows > 0 ? s.total_rows % p.rows : 0}) {
+      const int32_t rc = static_cast<int32_t>(rows);
+      p.mla_bytes = std::max(p.mla_bytes, mla_ws_bytes(d, paged_splits(d, s, rc, sm_count), rc));
+    }
   } else {
     const int32_t* cu = s.cu_seqlens_host;
     int64_t max_rows = 0;
@@ -696,23 +839,25 @@ dsa_status_t kl_backward_launch(bool full, const IdxBwdParams& prm, cudaStream_t
 dsa_status_t forward_window(const dsa_dims_t& d, const dsa_seqs_t& s, int64_t w0, int64_t w1,
                             const uint8_t* q_idx, const float* q_scale, const float* w,
                             const uint8_t* k_idx, const float* k_scale, const uint16_t* q,
-                            const uint16_t* kv, int32_t* idx_out, float* sel_out, uint16_t* out,
+                            const void* kv_rows, int32_t* idx_out, float* sel_out, uint16_t* out,
                             float* lse, void* workspace, size_t workspace_bytes,
-                            int32_t* dev_status, cudaStream_t st) {
+                            int32_t* dev_status, cudaStream_t st, bool q8 = false) {
   dsa_status_t e;
+  const uint16_t* kv = static_cast<const uint16_t*>(kv_rows);   // (q8: only kv_rows is used)
   if (!indexer_shape_ok(d, s.mode) || !mla_shape_ok(d)) return DSA_ERR_UNSUPPORTED_SHAPE;
-  if (!q_idx || !q_scale || !w || !k_idx || !q || !kv || !out || !lse)
+  if (!q_idx || !q_scale || !w || !k_idx || !q || !kv_rows || !out || !lse)
     return DSA_ERR_INVALID_ARG;
   if (sel_out != nullptr && idx_out == nullptr) return DSA_ERR_INVALID_ARG;
   if (k_scale == nullptr && !interleaved_ok(s)) return DSA_ERR_INVALID_ARG;
   if (!aligned16(q_idx) || !aligned16(k_idx) || !aligned16(k_scale) || !aligned16(q) ||
-      !aligned16(kv) || !aligned16(out) || !aligned16(lse) || !aligned16(idx_out) ||
+      !aligned16(kv_rows) || !aligned16(out) || !aligned16(lse) || !aligned16(idx_out) ||
       !aligned16(sel_out) || !aligned16(workspace) || !aligned16(q_scale) || !aligned16(w))
     return DSA_ERR_MISALIGNED;
   DeviceInfo info;
   if (device_info(&info) != DSA_OK) return DSA_ERR_CUDA;
-  const ForwardPlan plan = plan_forward(d, s, info.sm_count);
-  if (workspace == nullptr || workspace_bytes < plan.total) return DSA_ERR_WORKSPACE_TOO_SMALL;
+  const ForwardPlan plan = plan_forward(d, s, info.sm_count, q8);
+  if ((workspace == nullptr && plan.total > 0) || workspace_bytes < plan.total)
+    return DSA_ERR_WORKSPACE_TOO_SMALL;
   if (w1 <= w0) return DSA_OK;
   auto align = [](size_t x) { return (x + 255) / 256 * 256; };
   uint8_t* wsb = static_cast<uint8_t*>(workspace);
@@ -729,6 +874,26 @@ dsa_status_t forward_window(const dsa_dims_t& d, const dsa_seqs_t& s, int64_t w0
       cudaMemsetAsync(hist, 0, size_t(plan.hist_rows) * kTopkBins * 4, st) != cudaSuccess)
     return DSA_ERR_CUDA;
 
+  if (s.mode == DSA_CHUNK || q8) {
+    // chunks over either cache, decode over the 8-bit one: launches of at most plan.rows rows
+    const bool all_keys = idx_out == nullptr && s.max_seqlen <= d.topk;   // dense: no selection
+    for (int64_t r0 = w0; r0 < w1; r0 += plan.rows) {
+      const int32_t rb = static_cast<int32_t>(r0);
+      const int32_t rc = static_cast<int32_t>(std::min(plan.rows, w1 - r0));
+      int32_t* idx = all_keys ? nullptr : idx_out ? idx_out + r0 * d.topk : idx_ws;
+      float* sel = sel_out ? sel_out + r0 * d.topk : nullptr;
+      if (!all_keys &&
+          (e = indexer_topk(d, s, q_idx, q_scale, w, k_idx, k_scale, rb, rc, slab,
+                            round4(s.max_seqlen), hist, idx, sel, dev_status, st)) != DSA_OK)
+        return e;
+      // (a window of fewer rows may split more, as far as the planned partials allow)
+      const int splits = paged_splits(d, s, rc, info.sm_count, plan.mla_bytes);
+      if ((e = paged_mla_dispatch(d, s, q, kv_rows, q8, idx, rb, rc, out, lse, mla_ws,
+                                  mla_ws_bytes(d, splits, rc), dev_status, st, splits)) != DSA_OK)
+        return e;
+    }
+    return DSA_OK;
+  }
   if (s.mode == DSA_DECODE) {
     const int32_t rb = static_cast<int32_t>(w0), rc = static_cast<int32_t>(w1 - w0);
     // a window of fewer sequences may split more: as far as the planned partials allow
@@ -780,12 +945,49 @@ dsa_status_t forward_window(const dsa_dims_t& d, const dsa_seqs_t& s, int64_t w0
   return DSA_OK;
 }
 
+// ------------------------------------------------------------------- paged cache writes
+
+bool latent_shape_ok(const dsa_dims_t& d) {
+  return (d.d_qk == 576 && d.d_v == 512) || (d.d_qk == 160 && d.d_v == 128);
+}
+
+// New tokens (decode: one per sequence; chunk: several) into the key and latent caches.
+dsa_status_t cache_write(const dsa_dims_t& d, const dsa_seqs_t& s, const float* k_new,
+                         const uint16_t* kv_new, uint8_t* k_cache, float* k_scale,
+                         void* kv_cache, bool q8, int32_t* status, cudaStream_t st) {
+  const bool full = d.d_idx == 128 && d.d_qk == 576;
+  const bool tiny = d.d_idx == 32 && d.d_qk == 160;
+  if ((!full && !tiny) || !latent_shape_ok(d)) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (!k_new || !kv_new || !k_cache || !kv_cache) return DSA_ERR_INVALID_ARG;
+  if (k_scale == nullptr && !interleaved_ok(s)) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(kv_new) || !aligned16(k_cache) || !aligned16(k_scale) ||
+      !aligned16(kv_cache))
+    return DSA_ERR_MISALIGNED;
+  if (s.total_rows == 0) return DSA_OK;
+  CacheWriteParams prm{};
+  prm.s = paged_seqs(s);
+  prm.k_new = k_new;
+  prm.kv_new = reinterpret_cast<const uint8_t*>(kv_new);
+  prm.k_cache = k_cache;
+  prm.k_scale = k_scale;
+  prm.kv_cache = static_cast<uint8_t*>(kv_cache);
+  prm.total_rows = s.total_rows;
+  prm.status = status;
+  const unsigned grid = static_cast<unsigned>(ceil_div(s.total_rows, 4));
+  if (full && q8) dsa_cache_write_kernel<128, 576, 512, true><<<grid, 128, 0, st>>>(prm);
+  else if (full) dsa_cache_write_kernel<128, 576, 512, false><<<grid, 128, 0, st>>>(prm);
+  else if (q8) dsa_cache_write_kernel<32, 160, 128, true><<<grid, 128, 0, st>>>(prm);
+  else dsa_cache_write_kernel<32, 160, 128, false><<<grid, 128, 0, st>>>(prm);
+  return launch_status();
+}
+
 // ------------------------------------------------------------------- training entry bodies
 
 dsa_status_t kl_target_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint16_t* q,
                             const uint16_t* kv, const int32_t* idx, const float* lse,
                             int32_t row_begin, int32_t row_count, float* target,
                             int64_t ld_target, int32_t* status, cudaStream_t st) {
+  if (s.mode == DSA_CHUNK) return DSA_ERR_INVALID_ARG;
   if (!mla_shape_ok(d)) return DSA_ERR_UNSUPPORTED_SHAPE;
   dsa_status_t e;
   if ((e = check_rows(&s, row_begin, row_count)) != DSA_OK) return e;
@@ -810,6 +1012,7 @@ dsa_status_t kl_backward_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const ui
                               int64_t ld_target, int32_t row_begin, int32_t row_count,
                               float* loss, float* dw, float* dq, float* dk, int32_t* status,
                               cudaStream_t st) {
+  if (s.mode == DSA_CHUNK) return DSA_ERR_INVALID_ARG;
   const bool full = d.h_idx == 64 && d.d_idx == 128;
   const bool tiny = d.h_idx == 4 && d.d_idx == 32;
   if (!full && !tiny) return DSA_ERR_UNSUPPORTED_SHAPE;
@@ -1129,7 +1332,8 @@ size_t dsa_forward_workspace_size_for(const dsa_dims_t* dims, const dsa_seqs_t* 
 int32_t dsa_forward_chunk_rows_for(const dsa_dims_t* dims, const dsa_seqs_t* seqs, int32_t seq,
                                    int32_t sm_count) {
   if (check_common(dims, seqs) != DSA_OK || sm_count <= 0) return 0;
-  if (seqs->mode != DSA_PREFILL) return seqs->batch;
+  if (seqs->mode == DSA_DECODE) return seqs->batch;
+  if (seqs->mode == DSA_CHUNK) return static_cast<int32_t>(paged_rows_for(*seqs, sm_count));
   if (seq < 0 || seq >= seqs->batch) return 0;
   const int64_t L = seqs->cu_seqlens_host[seq + 1] - seqs->cu_seqlens_host[seq];
   return L <= 0 ? 0 : static_cast<int32_t>(chunk_rows_for(L, sm_count));
@@ -1202,7 +1406,10 @@ dsa_status_t dsa_cache_append(const dsa_dims_t* dims, const dsa_seqs_t* seqs, co
   if (e != DSA_OK) return e;
   const dsa_dims_t& d = *dims;
   const dsa_seqs_t& s = *seqs;
-  if (s.mode != DSA_DECODE) return DSA_ERR_INVALID_ARG;
+  if (s.mode == DSA_PREFILL) return DSA_ERR_INVALID_ARG;
+  if (s.mode == DSA_CHUNK)
+    return cache_write(d, s, k_new, kv_new, k_cache, k_scale_cache, kv_cache, false, dev_status,
+                       reinterpret_cast<cudaStream_t>(stream));
   const bool full = d.d_idx == 128 && d.d_qk == 576;
   const bool tiny = d.d_idx == 32 && d.d_qk == 160;
   if (!full && !tiny) return DSA_ERR_UNSUPPORTED_SHAPE;
@@ -1232,6 +1439,106 @@ dsa_status_t dsa_cache_append(const dsa_dims_t* dims, const dsa_seqs_t* seqs, co
   else
     dsa_cache_append_kernel<32, 160><<<grid, 128, 0, st>>>(prm);
   return launch_status();
+}
+
+size_t dsa_q8_row_bytes(const dsa_dims_t* dims) {
+  if (dims == nullptr || !latent_shape_ok(*dims)) return 0;
+  return dims->d_qk == 576 ? Q8Row<576, 512>::BYTES : Q8Row<160, 128>::BYTES;
+}
+
+dsa_status_t dsa_cache_append_q8(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
+                                 const float* k_new, const uint16_t* kv_new, uint8_t* k_cache,
+                                 float* k_scale_cache, uint8_t* kv8_cache, int32_t* dev_status,
+                                 dsa_stream_t stream) {
+  NvtxRange nvtx_range("dsa_cache_append_q8");
+  dsa_status_t e = check_common(dims, seqs);
+  if (e != DSA_OK) return e;
+  if (seqs->mode == DSA_PREFILL) return DSA_ERR_INVALID_ARG;
+  return cache_write(*dims, *seqs, k_new, kv_new, k_cache, k_scale_cache, kv8_cache, true,
+                     dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t dsa_cache_read_q8(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
+                               const uint8_t* kv8_cache, const int32_t* key_begin,
+                               const int32_t* cu_keys, int32_t total_keys, uint16_t* kv_out,
+                               int32_t* dev_status, dsa_stream_t stream) {
+  NvtxRange nvtx_range("dsa_cache_read_q8");
+  dsa_status_t e = check_common(dims, seqs);
+  if (e != DSA_OK) return e;
+  if (seqs->mode == DSA_PREFILL || total_keys < 0) return DSA_ERR_INVALID_ARG;
+  if (!latent_shape_ok(*dims)) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (!kv8_cache || !cu_keys || !kv_out) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(kv8_cache) || !aligned16(key_begin) || !aligned16(cu_keys) || !aligned16(kv_out))
+    return DSA_ERR_MISALIGNED;
+  if (total_keys == 0) return DSA_OK;
+  CacheReadParams prm{};
+  prm.s = paged_seqs(*seqs);
+  prm.kv8 = kv8_cache;
+  prm.key_begin = key_begin;
+  prm.cu_keys = cu_keys;
+  prm.out = reinterpret_cast<uint8_t*>(kv_out);
+  prm.total_keys = total_keys;
+  prm.status = dev_status;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned grid = static_cast<unsigned>(ceil_div(total_keys, 8));
+  if (dims->d_qk == 576)
+    dsa_cache_read_kernel<576, 512><<<grid, 256, 0, st>>>(prm);
+  else
+    dsa_cache_read_kernel<160, 128><<<grid, 256, 0, st>>>(prm);
+  return launch_status();
+}
+
+size_t dsa_sparse_mla_q8_workspace_size(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
+                                        int32_t row_count) {
+  if (check_common(dims, seqs) != DSA_OK) return 0;
+  DeviceInfo info;
+  if (device_info(&info) != DSA_OK) return 0;
+  return mla_ws_bytes(*dims, paged_splits(*dims, *seqs, row_count, info.sm_count), row_count);
+}
+
+dsa_status_t dsa_sparse_mla_fwd_q8(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
+                                   const uint16_t* q, const uint8_t* kv8, const int32_t* idx,
+                                   int32_t row_begin, int32_t row_count, uint16_t* out,
+                                   float* lse, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_status, dsa_stream_t stream) {
+  NvtxRange nvtx_range("dsa_sparse_mla_fwd_q8");
+  dsa_status_t e = check_common(dims, seqs);
+  if (e != DSA_OK) return e;
+  if (seqs->mode == DSA_PREFILL) return DSA_ERR_INVALID_ARG;
+  if (!mla_shape_ok(*dims)) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if ((e = check_rows(seqs, row_begin, row_count)) != DSA_OK) return e;
+  if (!q || !kv8 || !out || !lse) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(kv8) || !aligned16(idx) || !aligned16(out) || !aligned16(lse) ||
+      !aligned16(workspace))
+    return DSA_ERR_MISALIGNED;
+  DeviceInfo info;
+  if (device_info(&info) != DSA_OK) return DSA_ERR_CUDA;
+  const int splits = paged_splits(*dims, *seqs, row_count, info.sm_count);
+  return paged_mla_dispatch(*dims, *seqs, q, kv8, true, idx, row_begin, row_count, out, lse,
+                            workspace, workspace_bytes, dev_status,
+                            reinterpret_cast<cudaStream_t>(stream), splits);
+}
+
+size_t dsa_forward_q8_workspace_size(const dsa_dims_t* dims, const dsa_seqs_t* seqs) {
+  if (check_common(dims, seqs) != DSA_OK || seqs->mode == DSA_PREFILL) return 0;
+  DeviceInfo info;
+  if (device_info(&info) != DSA_OK) return 0;
+  return plan_forward(*dims, *seqs, info.sm_count, true).total;
+}
+
+dsa_status_t dsa_forward_q8(const dsa_dims_t* dims, const dsa_seqs_t* seqs, const uint8_t* q_idx,
+                            const float* q_scale, const float* w, const uint8_t* k_idx,
+                            const float* k_scale, const uint16_t* q, const uint8_t* kv8,
+                            int32_t* idx_out, float* sel_out, uint16_t* out, float* lse,
+                            void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                            dsa_stream_t stream) {
+  NvtxRange nvtx_range("dsa_forward_q8");
+  dsa_status_t e = check_common(dims, seqs);
+  if (e != DSA_OK) return e;
+  if (seqs->mode == DSA_PREFILL) return DSA_ERR_INVALID_ARG;
+  return forward_window(*dims, *seqs, 0, seqs->total_rows, q_idx, q_scale, w, k_idx, k_scale, q,
+                        kv8, idx_out, sel_out, out, lse, workspace, workspace_bytes, dev_status,
+                        reinterpret_cast<cudaStream_t>(stream), true);
 }
 
 dsa_status_t dsa_indexer_kl_target(const dsa_dims_t* dims, const dsa_seqs_t* seqs,

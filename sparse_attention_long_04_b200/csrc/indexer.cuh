@@ -29,7 +29,7 @@
 // adds the non-zero bins into the row's global histogram.  The top-k then starts from exact
 // per-row counts and classifies the slab in a single pass.
 #pragma once
-#include "sm100.cuh"
+#include "rows.cuh"
 
 namespace dsa {
 
@@ -56,6 +56,9 @@ struct IndexerParams {
   int64_t num_kv_rows;
   int32_t tiles_per_split;
   uint32_t* hist;         // optional: [slab rows][kIdxHistBins] first-digit counts (added to)
+  // chunk: query groups of every sequence of rows [row0, row0 + nrows), paged keys as in decode
+  const int32_t* cu_seqlens;
+  int32_t batch;
 };
 
 constexpr int kIdxHistBins = 2048;   // top 11 bits of the order-preserving score key
@@ -67,13 +70,13 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-template <int H_I, int D_I, int QPG>
+template <int H_I, int D_I, int QPG, bool kChunk = false>
 struct IndexerCfg {
   static constexpr int N = H_I * QPG;                 // MMA N: (row, head) columns
   static constexpr int STAGES = QPG == 1 ? 5 : 8;
-  // decode streams its keys from two producer warps (tiles of even and odd index), which keeps
+  // paged keys (decode, chunks) stream from two producer warps (tiles of even and odd index), which keeps
   // more page copies moving than one issuing thread does
-  static constexpr int PRODUCERS = QPG == 1 ? 2 : 1;
+  static constexpr int PRODUCERS = QPG == 1 || kChunk ? 2 : 1;
   static constexpr int ACC = QPG == 1 ? 4 : 2;        // TMEM accumulator ring
   static constexpr int EPI_WARPS = QPG == 1 ? 8 : 16;    // prefill: one query row per warpgroup
   static constexpr bool TILE_SPLIT = QPG == 1;        // warpgroups take alternate tiles
@@ -98,11 +101,45 @@ struct IndexerCfg {
   static_assert(Q_BYTES % 1024 == 0 && TILE_BYTES % 1024 == 0, "1024-byte aligned tiles");
 };
 
-template <int H_I, int D_I, int QPG>
-__global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG>::THREADS, QPG == 1 ? 2 : 1)
+// The query group of CTA x of a chunk launch: groups of QPG rows of one sequence, numbered
+// sequence by sequence over rows [row0, row0 + nrows).  One warp; every lane returns the group's
+// sequence, first row and row count (0: no such group).
+template <int QPG>
+__device__ __forceinline__ int3 chunk_group(const IndexerParams& p, int x, int lane) {
+  int3 g = make_int3(0, 0, 0);
+  for (int base = 0; base < p.batch; base += 32) {
+    const int b = base + lane;
+    int lo = 0, n = 0, groups = 0;
+    if (b < p.batch) {
+      lo = max(p.cu_seqlens[b], p.row0);
+      n = min(p.cu_seqlens[b + 1], p.row0 + p.nrows) - lo;
+      groups = n > 0 ? (n + QPG - 1) / QPG : 0;
+    }
+    int upto = groups;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, upto > x);
+    if (past != 0) {
+      const int src = __ffs(past) - 1;
+      const int k = x - (upto - groups);           // (meaningful in lane src)
+      g.x = __shfl_sync(0xffffffffu, b, src);
+      g.y = __shfl_sync(0xffffffffu, lo + k * QPG, src);
+      g.z = __shfl_sync(0xffffffffu, min(QPG, n - k * QPG), src);
+      return g;
+    }
+    x -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return g;
+}
+
+template <int H_I, int D_I, int QPG, bool kChunk = false>
+__global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QPG == 1 ? 2 : 1)
     dsa_indexer_kernel(const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap qmap, const IndexerParams p) {
-  using C = IndexerCfg<H_I, D_I, QPG>;
+  using C = IndexerCfg<H_I, D_I, QPG, kChunk>;
   constexpr int N = C::N;
   wait_prior_grid();   // (launched early: anything before it in the stream is complete here)
   extern __shared__ uint8_t smem_raw[];
@@ -137,7 +174,25 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG>::THREADS, QPG == 1 ?
   int n_keys, grow0, rows_in_group, pos_first;
   int64_t seq_base = 0;   // decode contiguous: first physical row of the sequence
   int b = 0;
-  if (p.decode) {
+  if constexpr (kChunk) {
+    __shared__ int3 group_s;
+    if (warp == 0) {
+      const int3 g = chunk_group<QPG>(p, static_cast<int>(blockIdx.x), lane);
+      if (lane == 0) group_s = g;
+    }
+    __syncthreads();
+    b = group_s.x;
+    grow0 = group_s.y;
+    rows_in_group = group_s.z;
+    if (rows_in_group <= 0) return;
+    const int len = p.seq_lens[b], ahead = p.cu_seqlens[b + 1] - grow0;
+    if ((len > p.max_seqlen || len < ahead) && threadIdx.x == 0 && p.status)
+      atomicOr(p.status, kStatusBadIndex);
+    pos_first = min(len, p.max_seqlen) - ahead;
+    n_keys = pos_first + rows_in_group;
+    seq_base = static_cast<int64_t>(b) * p.kv_stride;
+    if (n_keys <= 0) return;
+  } else if (p.decode) {
     b = p.row0 + blockIdx.x;
     n_keys = p.seq_lens[b];
     if (n_keys > p.max_seqlen) {
@@ -221,7 +276,7 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG>::THREADS, QPG == 1 ?
         const int tile = t_begin + it;
         float* sbuf = sScale + s * C::SCALE_FLOATS;
         uint32_t bytes;
-        if (!p.decode) {
+        if (!kChunk && !p.decode) {
           // prefill: the tile's 128 keys are contiguous rows; one box and one scale copy
           const int64_t y = static_cast<int64_t>(p.key0) + tile * 128;
           const int64_t a0 = y & ~int64_t(3);
@@ -269,11 +324,17 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG>::THREADS, QPG == 1 ?
             for (int hlf = 0; hlf < 2; ++hlf) {
               if (!ok[hlf]) continue;
               const int64_t blk = y[hlf] / 64;
-              tma_load_3d_hint(smem_u32(sK + s * C::TILE_BYTES + hlf * 64 * D_I), &kmap,
-                               smem_u32(&full[s]), 0, 0, static_cast<int32_t>(blk), pol);
-              bulk_load_g2s_hint(smem_u32(sbuf + hlf * 80),
-                                 p.k_blocks + blk * kBlockBytes + 64 * D_I, 256,
-                                 smem_u32(&full[s]), pol);
+              const uint32_t kdst = smem_u32(sK + s * C::TILE_BYTES + hlf * 64 * D_I);
+              const uint8_t* scales = p.k_blocks + blk * kBlockBytes + 64 * D_I;
+              if constexpr (kChunk) {              // other groups read the same pages: keep them
+                tma_load_3d(kdst, &kmap, smem_u32(&full[s]), 0, 0, static_cast<int32_t>(blk));
+                bulk_load_g2s(smem_u32(sbuf + hlf * 80), scales, 256, smem_u32(&full[s]));
+              } else {
+                tma_load_3d_hint(kdst, &kmap, smem_u32(&full[s]), 0, 0, static_cast<int32_t>(blk),
+                                 pol);
+                bulk_load_g2s_hint(smem_u32(sbuf + hlf * 80), scales, 256, smem_u32(&full[s]),
+                                   pol);
+              }
             }
           } else {
           // each box's 64 scales: a 16-byte-aligned superset of the rows, inside the cache
@@ -291,12 +352,21 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG>::THREADS, QPG == 1 ?
           bytes = (ok[0] ? 64 * D_I : 0) + (ok[1] ? 64 * D_I : 0) + sb[0] + sb[1];
           mbar_arrive_expect_tx(smem_u32(&full[s]), bytes);
           for (int hlf = 0; hlf < 2; ++hlf) {
-            if (ok[hlf])
-              tma_load_2d_hint(smem_u32(sK + s * C::TILE_BYTES + hlf * 64 * D_I), &kmap,
-                               smem_u32(&full[s]), 0, static_cast<int32_t>(y[hlf]), pol);
-            if (sb[hlf] > 0)
-              bulk_load_g2s_hint(smem_u32(sbuf + hlf * 80), p.k_scale + a0[hlf], sb[hlf],
-                                 smem_u32(&full[s]), pol);
+            const uint32_t kdst = smem_u32(sK + s * C::TILE_BYTES + hlf * 64 * D_I);
+            if constexpr (kChunk) {
+              if (ok[hlf])
+                tma_load_2d(kdst, &kmap, smem_u32(&full[s]), 0, static_cast<int32_t>(y[hlf]));
+              if (sb[hlf] > 0)
+                bulk_load_g2s(smem_u32(sbuf + hlf * 80), p.k_scale + a0[hlf], sb[hlf],
+                              smem_u32(&full[s]));
+            } else {
+              if (ok[hlf])
+                tma_load_2d_hint(kdst, &kmap, smem_u32(&full[s]), 0, static_cast<int32_t>(y[hlf]),
+                                 pol);
+              if (sb[hlf] > 0)
+                bulk_load_g2s_hint(smem_u32(sbuf + hlf * 80), p.k_scale + a0[hlf], sb[hlf],
+                                   smem_u32(&full[s]), pol);
+            }
           }
           }
         }

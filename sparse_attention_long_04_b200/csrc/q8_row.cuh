@@ -1,0 +1,93 @@
+// A row of the 8-bit latent cache and its arithmetic, shared by the kernels that write, read and
+// attend over it.
+//
+// Layout of one row (D_QK latent dims, the first D_V of them values):
+//   bytes [0, D_V)                     e4m3 codes of the D_V latent values
+//   bytes [D_V, D_V + S)               fp32 scales, one per group of 128 values; S = 4 bytes a
+//                                      group rounded up to 16 (unused scale slots are 0)
+//   bytes [D_V + S, ...)               the D_QK - D_V rotary dims in bf16, unquantised
+// 656 bytes at (576, 512), 208 at (160, 128): multiples of 16, so every part of every row is
+// 16-byte aligned.
+//
+// Scales are powers of two: s = 2^e with the smallest e such that max|x| <= 448 s (1 for a group
+// of zeros), e clamped to [-100, 119].  A code has 4 significant bits, so code * 2^e is exact in
+// bf16 (and fp32): reading back and attending never round, and the only rounding of the format is
+// x / s to the nearest e4m3 value (x / s itself is exact).  A floating-point code loses nothing
+// to the coarser scale but up to one binade of its 18.  A group that holds an infinity or a NaN
+// gets a NaN scale and zero codes, so that it reads back as NaN everywhere.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "sm100.cuh"
+
+namespace dsa {
+
+constexpr int kQ8Group = 128;       // values per scale
+constexpr int kQ8ExpMin = -100, kQ8ExpMax = 119;
+
+template <int D_QK, int D_V>
+struct Q8Row {
+  static_assert(D_V % kQ8Group == 0 && D_QK > D_V && (D_QK - D_V) % 8 == 0, "row dims");
+  static constexpr int GROUPS = D_V / kQ8Group;
+  static constexpr int ROPE = D_QK - D_V;
+  static constexpr int SCALE_OFF = D_V;
+  static constexpr int ROPE_OFF = D_V + (4 * GROUPS + 15) / 16 * 16;
+  static constexpr int BYTES = ROPE_OFF + 2 * ROPE;
+  static_assert(BYTES % 16 == 0, "16-byte rows");
+};
+
+// fp32 bits of 2^e, e in [-126, 127].
+__device__ __forceinline__ float exp2_int(int e) {
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Exponent of the scale of a group whose largest |x| has the bf16 bits `amax` (finite):
+// 448 = 1.75 * 2^8, so amax = (1 + m / 128) 2^E needs e = E - 8, one more when its mantissa is
+// above 1.75 (m > 96).
+__device__ __forceinline__ int q8_exponent(uint32_t amax) {
+  if (amax == 0) return 0;
+  const int e = static_cast<int>(amax >> 7) - 127 - 8 + ((amax & 0x7Fu) > 96u ? 1 : 0);
+  return min(max(e, kQ8ExpMin), kQ8ExpMax);
+}
+
+// The e4m3 code nearest to y (ties to even, saturating at +-448; y is finite).
+__device__ __forceinline__ uint32_t q8_code(float y) {
+  return __nv_cvt_float_to_fp8(fminf(fmaxf(y, -448.f), 448.f), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Four e4m3 codes (one per byte of w) times a power of two, as four bf16 (two per word).  A
+// code's sign, 4 exponent and 3 mantissa bits, moved to the sign and the bits 10..4 of a bf16,
+// are the code's value times 2^-120 (subnormal codes become bf16 subnormals); mul = 2^120 s in
+// both halves undoes it exactly.  Five instructions for two codes.
+__device__ __forceinline__ uint2 q8_expand4(uint32_t w, __nv_bfloat162 mul) {
+  const uint32_t a = __byte_perm(w, 0, 0x1404);   // codes 0, 1 in the high bytes of the halves
+  const uint32_t b = __byte_perm(w, 0, 0x3424);   // codes 2, 3
+  const uint32_t ua = (a & 0x80008000u) | ((a >> 4) & 0x07F007F0u);
+  const uint32_t ub = (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u);
+  const __nv_bfloat162 pa = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&ua), mul);
+  const __nv_bfloat162 pb = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&ub), mul);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&pa), *reinterpret_cast<const uint32_t*>(&pb));
+}
+
+// Sixteen codes (one 16-byte chunk of a group with scale s) as sixteen bf16.  2^120 s is a bf16
+// up to s = 2^7; larger scales (and the NaN scale) multiply in two steps.
+__device__ __forceinline__ void q8_expand16(const uint4& c, float s, uint4& lo, uint4& hi) {
+  const bool big = !(s <= 128.f);                 // also the NaN scale
+  const float m1 = (big ? 128.f : s) * 0x1p120f;
+  const __nv_bfloat162 mul = __float2bfloat162_rn(m1);
+  uint2 e[4] = {q8_expand4(c.x, mul), q8_expand4(c.y, mul), q8_expand4(c.z, mul),
+                q8_expand4(c.w, mul)};
+  if (big) {
+    const __nv_bfloat162 m2 = __float2bfloat162_rn(s * 0x1p-7f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&e[i].x), m2);
+      const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&e[i].y), m2);
+      e[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    }
+  }
+  lo = make_uint4(e[0].x, e[0].y, e[1].x, e[1].y);
+  hi = make_uint4(e[2].x, e[2].y, e[3].x, e[3].y);
+}
+
+}  // namespace dsa

@@ -29,7 +29,7 @@
 // The scores are read from global memory once (twice without a given histogram, three times in
 // the crowded case), never held in shared memory.
 #pragma once
-#include "sm100.cuh"
+#include "rows.cuh"
 
 namespace dsa {
 
@@ -50,6 +50,7 @@ struct TopkParams {
   int32_t slice;           // keys per CTA slice (a multiple of 128), sizes the bitmaps
   uint32_t* hist;          // optional [row_count][kTopkBins] first-digit counts of each row's
                            // scores; read, then zeroed for the next use
+  int32_t chunk;           // rows of paged chunks: position from cu_seqlens and seq_lens
 };
 
 constexpr int kTopkThreads = 512;
@@ -254,7 +255,14 @@ __global__ void __launch_bounds__(kTopkThreads, 2) dsa_topk_kernel(const TopkPar
     hreg[3] = h4.w;
   }
   int n;
-  if (p.decode) {
+  if (p.chunk) {
+    const PagedSeqs s{1, p.batch, p.cu_seqlens, p.seq_lens, nullptr, 0, p.max_seqlen, 0};
+    int b, pos;
+    bool bad;
+    paged_row(s, row, &b, &pos, &bad);
+    if (bad && tid == 0 && crank == 0 && p.status) atomicOr(p.status, kStatusBadIndex);
+    n = static_cast<int>(min(static_cast<int64_t>(pos) + 1, p.ld));
+  } else if (p.decode) {
     n = p.seq_lens[row];
     if (n > p.max_seqlen || n > p.ld) {     // caller error: clamp to the slab and report
       if (tid == 0 && crank == 0 && p.status) atomicOr(p.status, kStatusBadIndex);
