@@ -328,9 +328,11 @@ dsa_status_t indexer_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint8_
              DSA_OK) {
     return DSA_ERR_CUDA;
   }
-  // (a chunk's map ends with the row range: a partial last group reads zeros past it)
-  const uint64_t q_rows = s.mode == DSA_CHUNK ? uint64_t(row_begin) + row_count : s.total_rows;
-  if (make_map(&qmap, q_idx, q_rows * H_I, D_I, C::N) != DSA_OK) return DSA_ERR_CUDA;
+  // the query map covers the row range alone: dsa_forward_rows hands in a base moved back by
+  // row_begin rows, a partial last group reads zeros past the range
+  if (make_map(&qmap, q_idx + int64_t(row_begin) * H_I * D_I, uint64_t(row_count) * H_I, D_I,
+               C::N) != DSA_OK)
+    return DSA_ERR_CUDA;
   IndexerParams prm{};
   prm.q_scale = q_scale;
   prm.w = w;
@@ -346,6 +348,7 @@ dsa_status_t indexer_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint8_
   prm.max_seqlen = s.max_seqlen;
   prm.num_kv_rows = s.num_kv_rows;
   prm.hist = C::HIST ? hist : nullptr;
+  prm.q_row0 = row_begin;
   const int ctas_per_sm = C::TMEM_COLS == 512 ? 1 : 2;
   const int64_t target = int64_t(info.sm_count) * ctas_per_sm * 4;
   if (s.mode == DSA_DECODE) {
@@ -617,9 +620,10 @@ dsa_status_t mla_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint16_t* 
     prm.part_o = static_cast<float*>(ws);
     prm.part_lse = prm.part_o + size_t(splits) * row_count * d.h * D_V;
   }
-  // Q in 64-dim x 128-head boxes
+  // Q in 64-dim x 128-head boxes, a map of the row range alone
   CUtensorMap q_map;
-  if (make_row_map(&q_map, q, uint64_t(s.total_rows) * d.h, D_QK * 2, 128, 128) != DSA_OK)
+  if (make_row_map(&q_map, q + int64_t(row_begin) * d.h * D_QK, uint64_t(row_count) * d.h,
+                   D_QK * 2, 128, 128) != DSA_OK)
     return DSA_ERR_CUDA;
   auto k = dsa_sparse_mla_kernel<D_QK, D_V>;
   if (prepare_kernel(k, C::SMEM_BYTES) != DSA_OK) return DSA_ERR_CUDA;
@@ -639,7 +643,7 @@ dsa_status_t paged_mla_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint
                             const void* kv, const int32_t* idx, int32_t row_begin,
                             int32_t row_count, uint16_t* out, float* lse, void* ws,
                             size_t ws_bytes, int32_t* status, cudaStream_t st, int splits) {
-  using C = MlaCfg<D_QK, D_V>;
+  using C = PagedCfg<D_QK, D_V>;
   PagedMlaParams prm{};
   prm.s = paged_seqs(s);
   prm.kv = static_cast<const uint8_t*>(kv);
@@ -662,10 +666,11 @@ dsa_status_t paged_mla_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint
     prm.part_o = static_cast<float*>(ws);
     prm.part_lse = prm.part_o + size_t(splits) * row_count * d.h * D_V;
   }
-  // Q in 64-dim x h-head boxes, no further than the row range
+  // Q in 64-dim x h-head boxes: a map of the row range alone (dsa_forward_rows hands in a base
+  // moved back by row_begin rows, and no map may start outside the caller's array)
   CUtensorMap q_map;
-  if (make_row_map(&q_map, q, (uint64_t(row_begin) + row_count) * d.h, D_QK * 2, 128, d.h) !=
-      DSA_OK)
+  if (make_row_map(&q_map, q + int64_t(row_begin) * d.h * D_QK, uint64_t(row_count) * d.h, D_QK * 2,
+                   128, d.h) != DSA_OK)
     return DSA_ERR_CUDA;
   auto k = dsa_paged_mla_kernel<D_QK, D_V, kQ8>;
   if (prepare_kernel(k, C::SMEM_BYTES) != DSA_OK) return DSA_ERR_CUDA;
@@ -805,7 +810,8 @@ dsa_status_t target_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint16_
   prm.target = target;
   prm.ld_target = ld_target;
   CUtensorMap q_map;
-  if (make_row_map(&q_map, q, uint64_t(s.total_rows) * d.h, D_QK * 2, 128, 128) != DSA_OK)
+  if (make_row_map(&q_map, q + int64_t(row_begin) * d.h * D_QK, uint64_t(row_count) * d.h,
+                   D_QK * 2, 128, 128) != DSA_OK)
     return DSA_ERR_CUDA;
   auto k = dsa_sparse_mla_kernel<D_QK, D_V, true>;
   if (prepare_kernel(k, C::SMEM_BYTES) != DSA_OK) return DSA_ERR_CUDA;

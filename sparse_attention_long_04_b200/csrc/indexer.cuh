@@ -48,6 +48,7 @@ struct IndexerParams {
   // decode: rows [row0, row0 + nrows) are sequences row0.. (one row each)
   int32_t row0, nrows, pos0, key0;
   int32_t out_row0;       // slab row of `row0`
+  int32_t q_row0;         // row of the query map's first row
   const int32_t* seq_lens;
   const int32_t* block_table;
   int32_t max_blocks;
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
       if (pr == 0) {
         tma_prefetch_desc(&qmap);
         mbar_arrive_expect_tx(smem_u32(qbar), C::Q_BYTES);
-        tma_load_2d(smem_u32(sQ), &qmap, smem_u32(qbar), 0, grow0 * H_I);
+        tma_load_2d(smem_u32(sQ), &qmap, smem_u32(qbar), 0, (grow0 - p.q_row0) * H_I);
       }
       const int n_blocks = (n_keys + 63) / 64;
       for (int it = pr; it < n_tiles; it += C::PRODUCERS) {

@@ -22,7 +22,7 @@
 // scales are powers of two) and store them into the same swizzled tiles the bf16 gather fills
 // with cp.async; the rotary dims are bf16 in both caches and always come by cp.async.
 //
-// Warp roles (512 threads): warp 0 QK, warp 2 PV, warp 1 TMEM, warps 4-7 Q into TMEM, softmax and
+// Warp roles (512 threads): warp 0 issues the MMAs, warp 1 owns TMEM, warps 4-7 Q into TMEM, softmax and
 // epilogue (thread = head), warps 8-11 the K part and warps 12-15 the V part of every tile.
 // Without idx the keys are every prior key; a 64-key tile is then one page, and the pages of a
 // split's tiles are resolved up front (kMaxDenseTiles of them).
@@ -46,6 +46,43 @@ struct PagedMlaParams {
   int32_t* status;
 };
 
+// Rings of one CTA: the K part's value blocks in one slot (freed as soon as their MMAs have run,
+// refilled while the V part's run), the rotary block in two, the V part in three (a slot is held
+// until PV, and the next use needs it only when the third QK after comes to its V part).
+template <int D_QK, int D_V>
+struct PagedCfg {
+  static constexpr int KB_ALL = (D_QK + 63) / 64;     // 64-dim k-blocks of a latent row
+  static constexpr int V_HALF = D_V / 2;              // value dims per CTA
+  static constexpr int VKB = V_HALF / 64;             // value blocks per CTA (V part)
+  static constexpr int NK = KB_ALL - VKB - 1;         // value blocks of the other CTA (K part)
+  static constexpr int BN = 64;                       // keys per tile
+  static constexpr int R_SLOTS = 2, V_SLOTS = 3;
+  static constexpr int MAX_TILES = 32;                // topk <= 2048
+  static constexpr int THREADS = 512;
+  // TMEM: O, S, P (bf16), then the rotary and K-part blocks of Q and as many more as fit
+  static constexpr int S_COL = V_HALF;
+  static constexpr int P_COL = S_COL + BN;
+  static constexpr int Q_COL = P_COL + BN / 2;
+  static constexpr int KBT_MAX = (512 - Q_COL) / 32;
+  static constexpr int KBT = KB_ALL < KBT_MAX ? KB_ALL : KBT_MAX;   // Q blocks in TMEM
+  static constexpr int KBS = KB_ALL - KBT;                            // Q blocks in smem
+  static constexpr int TMEM_COLS = Q_COL + KBT * 32 <= 256 ? 256 : 512;
+  static constexpr int KB_BYTES = BN * 128;                           // one k-block of a tile
+  static constexpr int RING_BYTES = (NK + R_SLOTS + V_SLOTS * VKB) * KB_BYTES;
+  static constexpr int Q_KB_BYTES = 128 * 128;                        // one k-block of Q
+  static constexpr int Q_SMEM_BYTES = KBS * Q_KB_BYTES;
+  static constexpr int SMEM_USED = 1024 + Q_SMEM_BYTES + RING_BYTES + MAX_TILES * BN * 4 +
+                                   MAX_TILES * 12 + 256;
+  // at least 116 KB, so that one CTA runs per SM (its TMEM allocation never waits)
+  static constexpr int SMEM_BYTES = SMEM_USED > 116 * 1024 ? SMEM_USED : 116 * 1024;
+  static_assert(V_HALF % 64 == 0 && V_HALF <= 256, "PV MMA N");
+  static_assert(NK == VKB, "both parts hold as many value blocks");
+  static_assert(KBT >= NK + 1, "the K part's Q blocks live in TMEM");
+  static_assert(Q_COL + KBT * 32 <= 512, "TMEM columns");
+  static_assert(KBT * Q_KB_BYTES <= RING_BYTES, "Q staging fits the gather rings");
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+};
+
 constexpr int kMaxDenseTiles = 2048;   // tiles of one split without idx
 
 // True in one lane of the (converged) warp.
@@ -59,6 +96,34 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Whole-warp wait for phase `parity` of `bar`: every lane polls (one broadcast access) without a
+// suspend-time hint, which a completed phase answers in 14 cycles against 46 with the hint and 195
+// for warp_mbar_wait's poll by lane 0 and shuffle.  The clock and the abort flag are looked at
+// once in 64 polls; all lanes return the same result.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity,
+                                          const volatile int* abort) {
+  uint32_t ok = 0;
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t it = 1;; ++it) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) break;
+    if ((it & 63u) == 0) {
+      if (abort != nullptr && *abort) break;
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > kWaitLimitNs) break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
 // 2^x, results below the normal range flushed to 0 (a probability that small adds nothing).
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -70,34 +135,35 @@ __device__ __forceinline__ float exp2_approx(float x) {
 template <int D_QK, int D_V, bool kQ8>
 __global__ void __launch_bounds__(512, 1)
     dsa_paged_mla_kernel(const __grid_constant__ CUtensorMap q_map, const PagedMlaParams p) {
-  using C = MlaCfg<D_QK, D_V>;
+  using C = PagedCfg<D_QK, D_V>;
   using R = Q8Row<D_QK, D_V>;
   constexpr int ROW_BYTES = kQ8 ? R::BYTES : D_QK * 2;
-  static_assert(C::KBT >= C::KK, "the K part's Q blocks live in TMEM");
   static_assert(R::ROPE <= 64 && D_V % 64 == 0, "rotary dims fill (part of) the last k-block");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* sQ = smem;                                           // [KBS][128 heads][128 B]
   uint8_t* sRing = sQ + C::Q_SMEM_BYTES;                        // gather rings (Q staging first)
-  uint8_t* sK = sRing;                                          // [STAGES][KK k-blocks]
-  uint8_t* sV = sRing + C::STAGES * C::K_SLOT_BYTES;            // [STAGES][VKB k-blocks]
+  uint8_t* sK = sRing;                                          // [NK k-blocks]
+  uint8_t* sR = sK + C::NK * C::KB_BYTES;                       // [R_SLOTS] rotary k-blocks
+  uint8_t* sV = sR + C::R_SLOTS * C::KB_BYTES;                  // [V_SLOTS][VKB k-blocks]
   // selected: the physical row of every key; dense: the first physical row of every tile
   int32_t* sPhys = reinterpret_cast<int32_t*>(sRing + C::RING_BYTES);             // [2048]
   uint64_t* sMask = reinterpret_cast<uint64_t*>(sPhys + C::MAX_TILES * C::BN);   // [32]
   int32_t* sTiles = reinterpret_cast<int32_t*>(sMask + C::MAX_TILES);            // [32]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sTiles + C::MAX_TILES);
-  uint64_t* k_full = bars;           // [2] every K-part thread, once per way its data arrives
-  uint64_t* k_empty = bars + 2;      // [2] QK commit
-  uint64_t* v_full = bars + 4;       // [2] every V-part thread
-  uint64_t* v_empty = bars + 6;      // [2] PV commit
-  uint64_t* s_full = bars + 8;       // QK commit
-  uint64_t* s_empty = bars + 9;      // 4 softmax warps
-  uint64_t* p_full = bars + 10;      // 4 softmax warps
-  uint64_t* pv_done = bars + 11;     // PV commit
-  uint64_t* qk_fin = bars + 12;
-  uint64_t* pv_fin = bars + 13;
-  uint64_t* q_bar = bars + 14;       // 1 arrival + Q bytes
+  uint64_t* k_full = bars;           // every K-part thread
+  uint64_t* k_empty = bars + 1;      // commit of the K part's MMAs
+  uint64_t* r_full = bars + 2;       // [2] every K-part thread (rotary copies landed)
+  uint64_t* r_empty = bars + 4;      // [2] the same commit
+  uint64_t* v_full = bars + 6;       // [3] every V-part thread
+  uint64_t* v_empty = bars + 9;      // [3] PV commit
+  uint64_t* s_full = bars + 12;       // QK commit
+  uint64_t* s_empty = bars + 13;      // 4 softmax warps
+  uint64_t* p_full = bars + 14;      // 4 softmax warps
+  uint64_t* pv_done = bars + 15;     // PV commit
+  uint64_t* mma_fin = bars + 16;     // every MMA of this CTA completed
+  uint64_t* q_bar = bars + 17;       // 1 arrival + Q bytes
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
   __shared__ int n_act_s;
@@ -131,9 +197,13 @@ __global__ void __launch_bounds__(512, 1)
   if (bad_row && threadIdx.x == 0 && p.status) atomicOr(p.status, kStatusBadIndex);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(smem_u32(&k_full[i]), kQ8 ? 256 : 128);
-      mbar_init(smem_u32(&k_empty[i]), 1);
+    mbar_init(smem_u32(k_full), 128);
+    mbar_init(smem_u32(k_empty), 1);
+    for (int i = 0; i < C::R_SLOTS; ++i) {
+      mbar_init(smem_u32(&r_full[i]), 128);
+      mbar_init(smem_u32(&r_empty[i]), 1);
+    }
+    for (int i = 0; i < C::V_SLOTS; ++i) {
       mbar_init(smem_u32(&v_full[i]), 128);
       mbar_init(smem_u32(&v_empty[i]), 1);
     }
@@ -141,8 +211,7 @@ __global__ void __launch_bounds__(512, 1)
     mbar_init(smem_u32(s_empty), 4);
     mbar_init(smem_u32(p_full), 4);
     mbar_init(smem_u32(pv_done), 1);
-    mbar_init(smem_u32(qk_fin), 1);
-    mbar_init(smem_u32(pv_fin), 1);
+    mbar_init(smem_u32(mma_fin), 1);
     mbar_init(smem_u32(q_bar), 1);
     abort_s = 0;
     fence_mbar_init();
@@ -150,16 +219,18 @@ __global__ void __launch_bounds__(512, 1)
   if (warp == 1) tmem_alloc(smem_u32(&tmem_base_s), C::TMEM_COLS);
   __syncthreads();
   if (threadIdx.x == 0) {
-    // ---- Q, in the order K part, V part: KBT blocks into the (still idle) rings, the rest into
-    // sQ; h rows a block (lanes past h hold whatever the staging area held and are never written)
+    // ---- Q, in the order rotary, K part, V part: KBT blocks into the (still idle) rings, the rest
+    // into sQ; h rows a block (lanes past h hold whatever the staging area held and are never written)
     const uint32_t kb_bytes = static_cast<uint32_t>(p.h) * 128u;
     tma_prefetch_desc(&q_map);
     mbar_arrive_expect_tx(smem_u32(q_bar), C::KB_ALL * kb_bytes);
     for (int j = 0; j < C::KB_ALL; ++j) {
       const int v0 = vh * C::VKB;
-      const int kb = j >= C::KK ? v0 + j - C::KK : (j < v0 ? j : j + C::VKB);
+      const int kb = j == 0 ? C::KB_ALL - 1
+                   : j > C::NK ? v0 + j - 1 - C::NK
+                               : (j - 1 < v0 ? j - 1 : j - 1 + C::VKB);
       uint8_t* dst = j < C::KBT ? sRing + j * C::Q_KB_BYTES : sQ + (j - C::KBT) * C::Q_KB_BYTES;
-      tma_load_2d(smem_u32(dst), &q_map, smem_u32(q_bar), kb * 128, row * p.h);
+      tma_load_2d(smem_u32(dst), &q_map, smem_u32(q_bar), kb * 128, r * p.h);
     }
   }
   bool bad_idx = false;
@@ -247,7 +318,7 @@ __global__ void __launch_bounds__(512, 1)
     // Q_COL + d / 2
     const int hrow = (warp & 3) * 32 + lane;
     const uint32_t lane_addr = tmem_base_s + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    if (!(warp_mbar_wait(smem_u32(q_bar), 0, &abort_s))) {
+    if (!(warp_wait(smem_u32(q_bar), 0, &abort_s))) {
       abort_s = 1;
       if (p.status) atomicOr(p.status, kStatusTimeout);
     } else {
@@ -284,183 +355,191 @@ __global__ void __launch_bounds__(512, 1)
   };
 
   if (warp == 0) {
-    // ------------------------------------------------------------ QK issuer
-    constexpr uint32_t idesc = idesc_f32acc(1 /* bf16 */, 128, C::BN, 0, 0);
+    // ------------------------------------------------------------ MMA issuer
+    // QK(i) is issued before PV(i - 1), so that the tensor pipe runs PV(i - 1) while the softmax
+    // warps read S(i) out of its single buffer (and QK(i + 1) still has to wait for them).
+    constexpr uint32_t idesc_qk = idesc_f32acc(1 /* bf16 */, 128, C::BN, 0, 0);
+    constexpr uint32_t idesc_pv = idesc_f32acc(1, 128, C::V_HALF, 0, 1);
     const uint64_t qd = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    bool ok = n == 0 || warp_mbar_wait(smem_u32(q_bar), 0, &abort_s);
-    for (int i = 0; i < n && ok; ++i) {
-      const int s = i % C::STAGES;
-      const uint32_t ph = (i / C::STAGES) & 1;
-      const uint64_t kd = sdesc_sw128(smem_u32(sK + s * C::K_SLOT_BYTES), 16, 1024);
-      const uint64_t vd = sdesc_sw128(smem_u32(sV + s * C::V_SLOT_BYTES), 16, 1024);
-      ok = warp_mbar_wait(smem_u32(&k_full[s]), ph, &abort_s);
-      if (ok && i >= 1) ok = warp_mbar_wait(smem_u32(s_empty), (i - 1) & 1, &abort_s);
-      if (!ok) break;
-      tc_fence_after();
-      fence_proxy_async_smem();   // the rows were written by cp.async and ordinary stores
-      if (elect_one()) {
+    bool ok = n == 0 || warp_wait(smem_u32(q_bar), 0, &abort_s);
+    const uint64_t kd = sdesc_sw128(smem_u32(sK), 16, 1024);
+    int vs = 0, vs1 = 0;            // V slots of tiles i and i - 1
+    uint32_t vph = 0;
+    for (int i = 0; i <= n && ok; ++i) {
+      if (i < n) {
+        const int rs = i & 1;
+        const uint64_t rd = sdesc_sw128(smem_u32(sR + rs * C::KB_BYTES), 16, 1024);
+        const uint64_t vd = sdesc_sw128(smem_u32(sV + vs * (C::VKB * C::KB_BYTES)), 16, 1024);
+        ok = warp_wait(smem_u32(&r_full[rs]), (i >> 1) & 1, &abort_s) &&
+             warp_wait(smem_u32(k_full), i & 1, &abort_s) &&
+             (i == 0 || warp_wait(smem_u32(s_empty), (i - 1) & 1, &abort_s));
+        if (!ok) break;
+        tc_fence_after();
+        fence_proxy_async_smem();   // the rows were written by cp.async and ordinary stores
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 4 * C::KK; ++k)
-          umma_bf16_ts(tmem + C::S_COL, tmem + C::Q_COL + k * 8,
-                       kd + ((k / 4) * C::KB_BYTES + (k % 4) * 32) / 16, idesc, k != 0);
-      }
-      __syncwarp();
-      ok = warp_mbar_wait(smem_u32(&v_full[s]), ph, &abort_s);
-      if (!ok) break;
-      tc_fence_after();
-      fence_proxy_async_smem();
-      if (elect_one()) {
+          for (int k = 0; k < 4; ++k)
+            umma_bf16_ts(tmem + C::S_COL, tmem + C::Q_COL + k * 8, rd + k * 2, idesc_qk, k != 0);
 #pragma unroll
-        for (int k = 0; k < 4 * C::VKB; ++k) {
-          const int j = C::KK + k / 4;             // Q block
-          const uint64_t bd = vd + ((k / 4) * C::KB_BYTES + (k % 4) * 32) / 16;
-          if (j < C::KBT)
-            umma_bf16_ts(tmem + C::S_COL, tmem + C::Q_COL + j * 32 + (k % 4) * 8, bd, idesc, 1u);
-          else
-            umma_bf16(tmem + C::S_COL,
-                      qd + ((j - C::KBT) * C::Q_KB_BYTES + (k % 4) * 32) / 16, bd, idesc, 1u);
+          for (int k = 0; k < 4 * C::NK; ++k)
+            umma_bf16_ts(tmem + C::S_COL, tmem + C::Q_COL + 32 + k * 8,
+                         kd + ((k / 4) * C::KB_BYTES + (k % 4) * 32) / 16, idesc_qk, 1u);
+          umma_commit(smem_u32(k_empty));
+          umma_commit(smem_u32(&r_empty[rs]));
         }
-        umma_commit(smem_u32(s_full));
-        umma_commit(smem_u32(&k_empty[s]));
-      }
-      __syncwarp();
-    }
-    if (!ok) {
-      abort_s = 1;
-      if (lane == 0 && p.status) atomicOr(p.status, kStatusTimeout);
-    }
-    __syncwarp();
-    if (elect_one()) umma_commit(smem_u32(qk_fin));   // no MMA may outlive the CTA
-    __syncwarp();
-    warp_mbar_wait(smem_u32(qk_fin), 0, nullptr);
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ PV issuer
-    constexpr uint32_t idesc = idesc_f32acc(1, 128, C::V_HALF, 0, 1);
-    bool ok = true;
-    for (int i = 0; i < n && ok; ++i) {
-      const int s = i % C::STAGES;
-      const uint64_t vd = sdesc_sw128(smem_u32(sV + s * C::V_SLOT_BYTES), C::KB_BYTES, 1024);
-      ok = warp_mbar_wait(smem_u32(p_full), i & 1, &abort_s);
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
+        __syncwarp();
+        ok = warp_wait(smem_u32(&v_full[vs]), vph, &abort_s);
+        if (!ok) break;
+        tc_fence_after();
+        fence_proxy_async_smem();
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < C::BN / 16; ++k)
-          umma_bf16_ts(tmem, tmem + C::P_COL + k * 8, vd + k * 16 * 128 / 16, idesc,
-                       (i | k) != 0);
-        umma_commit(smem_u32(&v_empty[s]));
-        umma_commit(smem_u32(pv_done));
+          for (int k = 0; k < 4 * C::VKB; ++k) {
+            const int j = 1 + C::NK + k / 4;         // Q block
+            const uint64_t bd = vd + ((k / 4) * C::KB_BYTES + (k % 4) * 32) / 16;
+            if (j < C::KBT)
+              umma_bf16_ts(tmem + C::S_COL, tmem + C::Q_COL + j * 32 + (k % 4) * 8, bd, idesc_qk,
+                           1u);
+            else
+              umma_bf16(tmem + C::S_COL,
+                        qd + ((j - C::KBT) * C::Q_KB_BYTES + (k % 4) * 32) / 16, bd, idesc_qk, 1u);
+          }
+          umma_commit(smem_u32(s_full));
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      if (i > 0) {
+        const uint64_t vd = sdesc_sw128(smem_u32(sV + vs1 * (C::VKB * C::KB_BYTES)), C::KB_BYTES,
+                                        1024);
+        ok = warp_wait(smem_u32(p_full), (i - 1) & 1, &abort_s);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < C::BN / 16; ++k)
+            umma_bf16_ts(tmem, tmem + C::P_COL + k * 8, vd + k * 16 * 128 / 16, idesc_pv,
+                         i > 1 || k != 0);
+          umma_commit(smem_u32(&v_empty[vs1]));
+          umma_commit(smem_u32(pv_done));
+        }
+        __syncwarp();
+      }
+      vs1 = vs;
+      if (++vs == C::V_SLOTS) {
+        vs = 0;
+        vph ^= 1u;
+      }
     }
     if (!ok) {
       abort_s = 1;
       if (lane == 0 && p.status) atomicOr(p.status, kStatusTimeout);
     }
     __syncwarp();
-    if (elect_one()) umma_commit(smem_u32(pv_fin));
+    if (elect_one()) umma_commit(smem_u32(mma_fin));   // no MMA may outlive the CTA
     __syncwarp();
-    warp_mbar_wait(smem_u32(pv_fin), 0, nullptr);
+    warp_wait(smem_u32(mma_fin), 0, nullptr);
   } else if (warp >= 8) {
     // ------------------------------------------------------------ gather producers
-    // Warp 8 + 4 part + w fills rows [16w, 16w + 16) of each tile: part 0 the K part, part 1 the
-    // V part.
+    // Warp 8 + 4 part + w fills rows [16w, 16w + 16) of each tile: part 0 the K part (and the
+    // rotary block), part 1 the V part.
     const int part = (warp - 8) >> 2;
     const int pw = (warp - 8) & 3;
     const int ch = lane & 7;                    // 16-byte chunk of a 128-byte row block
     const int rsub = lane >> 3;                 // rows rsub, rsub + 4, rsub + 8, rsub + 12
-    uint64_t* full = part == 0 ? k_full : v_full;
-    uint64_t* empty = part == 0 ? k_empty : v_empty;
-    // part block ks of this CTA is latent block kb
-    auto kb_of = [&](int ks) { return part == 0 ? (ks < vh * C::VKB ? ks : ks + C::VKB)
-                                                : vh * C::VKB + ks; };
-    // bf16 16-byte chunks, straight from the cache (rotary dims past D_QK are zeros)
-    auto copy_block = [&](uint8_t* dst, const uint8_t* src, int rr, int valid_chunks) {
-      const bool in = ch < valid_chunks;
-      cp_async_16(smem_u32(dst) + sw128_offset(pw * 16 + rr, ch),
-                  in ? static_cast<const void*>(src + ch * 16) : static_cast<const void*>(p.kv),
-                  in ? 16u : 0u);
-    };
-    // 8-bit codes: NB code blocks of one row group, LPR lanes a row, RPW rows a pass
-    auto expand_blocks = [&](auto nb_c, uint8_t* dst, int i) {
-      constexpr int NB = decltype(nb_c)::value;
-      constexpr int NCH = 4 * NB;                            // 16-code chunks of the part
-      constexpr int LPR = NCH < 8 ? NCH : 8;
-      constexpr int RPW = 32 / LPR, PASS = 16 / RPW, CP = NCH / LPR;
-      static_assert(LPR * RPW == 32 && CP * LPR == NCH && PASS * RPW == 16, "chunk split");
-      const int cl = lane % LPR, rl = lane / LPR;
-      uint4 code[PASS][CP];
-      float scale[PASS][CP];
+    const int kb0 = (part == 0) == (vh == 0) ? C::VKB : 0;   // the part's first latent block
+    // a block of bf16 rows straight from the cache, its chunks past `valid` zeros
+    auto copy_block = [&](uint8_t* dst, int i, int byte, int valid) {
+      const bool in = ch < valid;
 #pragma unroll
-      for (int q = 0; q < PASS; ++q) {
-        const uint8_t* src = p.kv + phys_of(i, pw * 16 + q * RPW + rl) * ROW_BYTES;
-#pragma unroll
-        for (int c = 0; c < CP; ++c) {
-          const int chunk = c * LPR + cl;
-          const int kb = kb_of(chunk / 4);
-          code[q][c] = __ldg(reinterpret_cast<const uint4*>(src + kb * 64) + chunk % 4);
-          scale[q][c] = __ldg(reinterpret_cast<const float*>(src + R::SCALE_OFF) + kb / 2);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const int rr = pw * 16 + rsub + 4 * j;
+        const uint8_t* src = p.kv + phys_of(i, rr) * ROW_BYTES + byte + ch * 16;
+        cp_async_16(smem_u32(dst) + sw128_offset(rr, ch), in ? src : p.kv, in ? 16u : 0u);
       }
+    };
+    // 8-bit codes: lane = 16-code chunk lane % 4 of rows lane / 4 and lane / 4 + 8, every value block
+    // of the part.  Eight lanes, two neighbouring rows, then store to the eight different 16-byte
+    // columns of a swizzled tile (eight lanes on one row would meet two to a column: 8.1 instead
+    // of 4 wavefronts a store).  Two register sets take turns: the set just stored is loaded with
+    // the codes and scales of two tiles on, so that their latency (HBM's, where the cache is
+    // large) goes by under a whole tile.
+    constexpr int GP = (C::VKB + 1) / 2;         // scales of a row's part (128 values, 2 blocks)
+    struct CodeSet {
+      uint4 code[2][C::VKB];
+      float scale[2][GP];
+    };
+    const int cl = lane & 3, rl = pw * 16 + (lane >> 2);
+    auto load_set = [&](CodeSet& x, int i) {
 #pragma unroll
-      for (int q = 0; q < PASS; ++q)
+      for (int q = 0; q < 2; ++q) {
+        const uint8_t* src = p.kv + phys_of(i, rl + 8 * q) * ROW_BYTES;
 #pragma unroll
-        for (int c = 0; c < CP; ++c) {
-          const int chunk = c * LPR + cl;
-          const int rr = pw * 16 + q * RPW + rl;
-          uint8_t* at = dst + (chunk / 4) * C::KB_BYTES;
+        for (int g = 0; g < GP; ++g)
+          x.scale[q][g] = __ldg(reinterpret_cast<const float*>(src + R::SCALE_OFF) + kb0 / 2 + g);
+#pragma unroll
+        for (int ks = 0; ks < C::VKB; ++ks)
+          x.code[q][ks] = __ldg(reinterpret_cast<const uint4*>(src + (kb0 + ks) * 64) + cl);
+      }
+    };
+    auto store_set = [&](const CodeSet& x, uint8_t* dst) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int ks = 0; ks < C::VKB; ++ks) {
+          uint8_t* at = dst + ks * C::KB_BYTES;
           uint4 lo, hi;
-          q8_expand16(code[q][c], scale[q][c], lo, hi);
-          *reinterpret_cast<uint4*>(at + sw128_offset(rr, 2 * (chunk % 4))) = lo;
-          *reinterpret_cast<uint4*>(at + sw128_offset(rr, 2 * (chunk % 4) + 1)) = hi;
+          q8_expand16(x.code[q][ks], x.scale[q][ks / 2], lo, hi);
+          *reinterpret_cast<uint4*>(at + sw128_offset(rl + 8 * q, 2 * cl)) = lo;
+          *reinterpret_cast<uint4*>(at + sw128_offset(rl + 8 * q, 2 * cl + 1)) = hi;
         }
     };
     bool ok = true;
-    for (int i = 0; i < n && ok; ++i) {
-      const int s = i % C::STAGES;
-      if (i >= C::STAGES &&
-          !(warp_mbar_wait(smem_u32(&empty[s]), ((i / C::STAGES) - 1) & 1, &abort_s))) {
-        ok = false;
-        break;
-      }
-      uint8_t* dst = part == 0 ? sK + s * C::K_SLOT_BYTES : sV + s * C::V_SLOT_BYTES;
-      if constexpr (kQ8) {
-        if (part == 0) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int rr = rsub + 4 * j;
-            copy_block(dst + (C::KK - 1) * C::KB_BYTES,
-                       p.kv + phys_of(i, pw * 16 + rr) * ROW_BYTES + R::ROPE_OFF, rr, R::ROPE / 8);
-          }
-          cp_async_arrive_noinc(smem_u32(&full[s]));
-          expand_blocks(std::integral_constant<int, C::KK - 1>{}, dst, i);
-        } else {
-          expand_blocks(std::integral_constant<int, C::VKB>{}, dst, i);
-        }
-        fence_proxy_async_smem();              // this thread's stores, before the MMAs read them
-        mbar_arrive(smem_u32(&full[s]));
+    int vs = 0;
+    uint32_t vph = 1;                            // (the first use of each slot does not wait)
+    // tile i: its slot waited for, filled, and the barrier told
+    auto fill = [&](CodeSet& x, int i) -> bool {
+      uint8_t* dst;
+      uint64_t* full;
+      if (part == 0) {
+        const int rs = i & 1;
+        if (i >= C::R_SLOTS &&
+            !warp_wait(smem_u32(&r_empty[rs]), ((i >> 1) - 1) & 1, &abort_s))
+          return false;
+        copy_block(sR + rs * C::KB_BYTES, i, kQ8 ? R::ROPE_OFF : 2 * D_V, R::ROPE / 8);
+        cp_async_arrive_noinc(smem_u32(&r_full[rs]));
+        if (i >= 1 && !warp_wait(smem_u32(k_empty), (i - 1) & 1, &abort_s)) return false;
+        dst = sK;
+        full = k_full;
       } else {
-        const int nb = part == 0 ? C::KK : C::VKB;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int rr = rsub + 4 * j;
-          const uint8_t* src = p.kv + phys_of(i, pw * 16 + rr) * ROW_BYTES;
-#pragma unroll
-          for (int ks = 0; ks < (C::KK > C::VKB ? C::KK : C::VKB); ++ks) {
-            if (ks >= nb) break;
-            const int kb = kb_of(ks);
-            copy_block(dst + ks * C::KB_BYTES, src + kb * 128, rr, min(8, (D_QK - kb * 64) / 8));
-          }
+        if (i >= C::V_SLOTS && !warp_wait(smem_u32(&v_empty[vs]), vph, &abort_s)) return false;
+        dst = sV + vs * (C::VKB * C::KB_BYTES);
+        full = &v_full[vs];
+        if (++vs == C::V_SLOTS) {
+          vs = 0;
+          vph ^= 1u;
         }
-        cp_async_arrive_noinc(smem_u32(&full[s]));
       }
-      // the rows of the tile PREFETCH steps ahead into L2 (its slot is not free yet): one
-      // thread per row of the K-part warps, each CTA of the pair half of the row
-      if (part == 0 && i + C::PREFETCH < n && pw < 2) {
-        constexpr uint32_t kHalf = (ROW_BYTES / 2 + 15) / 16 * 16;
-        const int64_t row2 = phys_of(i + C::PREFETCH, pw * 32 + lane);
-        prefetch_l2(p.kv + row2 * ROW_BYTES + vh * kHalf, vh == 0 ? kHalf : ROW_BYTES - kHalf);
+      if constexpr (kQ8) {
+        store_set(x, dst);
+        fence_proxy_async_smem();              // this thread's stores, before the MMAs read them
+        mbar_arrive(smem_u32(full));
+        if (i + 2 < n) load_set(x, i + 2);
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < C::VKB; ++ks)
+          copy_block(dst + ks * C::KB_BYTES, i, (kb0 + ks) * 128, 8);
+        cp_async_arrive_noinc(smem_u32(full));
       }
+      return true;
+    };
+    CodeSet set0, set1;
+    if constexpr (kQ8) {
+      if (n > 0) load_set(set0, 0);
+      if (n > 1) load_set(set1, 1);
+    }
+    for (int i = 0; i < n && ok; i += 2) {
+      ok = fill(set0, i);
+      if (ok && i + 1 < n) ok = fill(set1, i + 1);
     }
     if (!ok) {
       abort_s = 1;
@@ -474,7 +553,7 @@ __global__ void __launch_bounds__(512, 1)
     float m_ref = -INFINITY, l_sum = 0.f;
     bool ok = !abort_s;
     for (int i = 0; i < n && ok; ++i) {
-      ok = (warp_mbar_wait(smem_u32(s_full), i & 1, &abort_s));
+      ok = (warp_wait(smem_u32(s_full), i & 1, &abort_s));
       if (!ok) break;
       tc_fence_after();
       uint32_t su[2][32];                       // S of keys [32 hh, 32 hh + 32)
@@ -485,10 +564,6 @@ __global__ void __launch_bounds__(512, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(s_empty));
       const uint64_t vmask = mask_of(i);
-      // the tile max of the unscaled logits (sigma log2 e > 0), as 8 independent partial maxima
-      float mm[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) mm[q] = -INFINITY;
       if (vmask != ~0ull) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -498,10 +573,19 @@ __global__ void __launch_bounds__(512, 1)
             if (!((vb >> j) & 1u)) su[hh][j] = 0xFF800000u;
         }
       }
+      // the tile max of the unscaled logits (sigma log2 e > 0), as 8 independent partial maxima
+      float mm[8];
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh)
+      for (int q = 0; q < 8; ++q) mm[q] = __uint_as_float(su[0][q]);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) mm[j & 7] = fmaxf(mm[j & 7], __uint_as_float(su[hh][j]));
+      for (int j = 8; j < 64; j += 16)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float x = __uint_as_float(su[(j + q) / 32][(j + q) % 32]);
+          const int j2 = j + 8 + q;
+          mm[q] = j2 < 64 ? fmaxf(fmaxf(mm[q], x), __uint_as_float(su[j2 / 32][j2 % 32]))
+                          : fmaxf(mm[q], x);
+        }
       const float m_tile =
           fmaxf(fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])),
                 fmaxf(fmaxf(mm[4], mm[5]), fmaxf(mm[6], mm[7]))) * p.scale_log2;
@@ -516,26 +600,28 @@ __global__ void __launch_bounds__(512, 1)
       }
       // p = 2^(sigma log2e s - m_ref); the denominator sums the fp32 probabilities, only the PV
       // operand is rounded (bf16: the MMA's operand type)
-      float rs[8];
+      // (two keys to an instruction: the scaling FMA and the sums are packed fp32 pairs)
+      float2 rs[4];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) rs[q] = 0.f;
-      const float sc = p.scale_log2, nm = -m_ref;
+      for (int q = 0; q < 4; ++q) rs[q] = make_float2(0.f, 0.f);
+      const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-m_ref, -m_ref);
       uint32_t pk[2][16];
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float p0 = exp2_approx(fmaf(__uint_as_float(su[hh][2 * e]), sc, nm));
-          const float p1 = exp2_approx(fmaf(__uint_as_float(su[hh][2 * e + 1]), sc, nm));
-          rs[(2 * e) & 7] += p0;
-          rs[(2 * e + 1) & 7] += p1;
-          const __nv_bfloat162 two = __floats2bfloat162_rn(p0, p1);
+          const float2 x = __ffma2_rn(make_float2(__uint_as_float(su[hh][2 * e]),
+                                                  __uint_as_float(su[hh][2 * e + 1])), sc2, nm2);
+          const float2 pr = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+          rs[e & 3] = __fadd2_rn(rs[e & 3], pr);
+          const __nv_bfloat162 two = __float22bfloat162_rn(pr);
           pk[hh][e] = *reinterpret_cast<const uint32_t*>(&two);
         }
-      l_sum += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+      const float2 r01 = __fadd2_rn(__fadd2_rn(rs[0], rs[1]), __fadd2_rn(rs[2], rs[3]));
+      l_sum += r01.x + r01.y;
       // P and O are free once PV(i-1) has completed
       if (i >= 1) {
-        ok = (warp_mbar_wait(smem_u32(pv_done), (i - 1) & 1, &abort_s));
+        ok = (warp_wait(smem_u32(pv_done), (i - 1) & 1, &abort_s));
         if (!ok) break;
         tc_fence_after();
         if (__any_sync(0xffffffffu, need)) {       // O to the new reference
@@ -564,7 +650,7 @@ __global__ void __launch_bounds__(512, 1)
     const bool write = hrow < p.h;
     const int64_t orow = static_cast<int64_t>(row) * p.h + hrow;
     if (ok && n > 0)
-      ok = (warp_mbar_wait(smem_u32(pv_done), (n - 1) & 1, &abort_s));
+      ok = (warp_wait(smem_u32(pv_done), (n - 1) & 1, &abort_s));
     tc_fence_after();
     const bool any = ok && n > 0 && !(l_sum <= 0.f);   // (a NaN sum stays visible)
     const float inv_l = any ? 1.f / l_sum : 0.f;

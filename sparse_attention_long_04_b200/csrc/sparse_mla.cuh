@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(512, 1)
     mbar_arrive_expect_tx(smem_u32(q_bar), C::KB_ALL * C::Q_KB_BYTES);
     for (int kb = 0; kb < C::KB_ALL; ++kb) {
       uint8_t* dst = kb < C::KBT ? sRing + kb * C::Q_KB_BYTES : sQ + (kb - C::KBT) * C::Q_KB_BYTES;
-      tma_load_2d(smem_u32(dst), &q_map, smem_u32(q_bar), kb * 128, row * p.h);
+      tma_load_2d(smem_u32(dst), &q_map, smem_u32(q_bar), kb * 128, r * p.h);
     }
   }
   if (warp >= 8 && !stream_dense) {
