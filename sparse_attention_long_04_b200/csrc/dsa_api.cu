@@ -134,6 +134,28 @@ dsa_status_t launch_pdl(Kernel k, dim3 grid, int threads, int smem, cudaStream_t
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
+// The same with clusters of two CTAs along x.
+template <typename Kernel, typename... Args>
+dsa_status_t launch_pdl_cluster2(Kernel k, dim3 grid, int threads, int smem, cudaStream_t st,
+                                 Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, k, args...) != cudaSuccess) return DSA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
 dsa_status_t launch_status() {
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
@@ -674,8 +696,8 @@ dsa_status_t paged_mla_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint
     return DSA_ERR_CUDA;
   auto k = dsa_paged_mla_kernel<D_QK, D_V, kQ8>;
   if (prepare_kernel(k, C::SMEM_BYTES) != DSA_OK) return DSA_ERR_CUDA;
-  if (launch_pdl(k, dim3(2 * row_count, splits), C::THREADS, C::SMEM_BYTES, st, q_map, prm) !=
-      DSA_OK)
+  if (launch_pdl_cluster2(k, dim3(2 * row_count, splits), C::THREADS, C::SMEM_BYTES, st, q_map,
+                          prm) != DSA_OK)
     return DSA_ERR_CUDA;
   if (splits > 1) {
     dsa_paged_combine_kernel<D_V><<<dim3(row_count, d.h), D_V / 4, 0, st>>>(prm);

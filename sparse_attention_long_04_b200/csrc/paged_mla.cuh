@@ -4,32 +4,46 @@
 //   l_s = sigma * q[t,h,:] . kv[s,:],  O[t,h,:] = sum_s softmax(l)_s kv[s, 0:D_V],
 //   LSE[t,h] = log sum_s exp(l_s),  s over the row's selected keys (idx) or all its keys
 //
-// Layout of the work: two CTAs per query row (and split of its tiles), CTA v accumulating the
-// value dims [v D_V/2, (v+1) D_V/2) in TMEM and computing the full logits of every 64-key tile
-// itself, so that the two exchange nothing.  The latent row's 64-dim k-blocks are ordered K part
-// (the blocks CTA v needs for the logits only, rotary dims last) then V part (its value blocks);
-// Q's blocks follow the same order, the first KBT of them in TMEM, the others in shared memory,
-// so that every MMA operand sits at a constant offset from a tile's base.
+// Layout of the work: a cluster of two CTAs per query row (and split of its tiles).  O of 128
+// heads x 512 values in fp32 is a whole SM's TMEM, so CTA c accumulates the value dims
+// [c D_V/2, (c+1) D_V/2) of all heads.  It holds the same half of every gathered key and nothing
+// else: over it it computes PARTIAL logits of all heads (the rotary dims are added by the two
+// CTAs on alternate tiles), keeps those of its own 64 heads and sends the other 64 heads' to its
+// partner, so that every logit is the sum of two halves.  Each CTA then runs the softmax of its
+// own heads only and puts their probabilities into both CTAs' shared memory, as the A operand of
+// both PV products.  Nothing is gathered, expanded, multiplied or exponentiated twice.  Per 64-key
+// tile a CTA sends 16 KB of logits (st.async) and 8 KB of probabilities (a bulk copy per 32 heads)
+// to its partner, counted in bytes on the receiver's barriers.
 //
-// Issue: one elected lane of a converged warp (elect.sync) issues each tile's MMAs from
-// precomputed descriptors.  Issued from an ordinary `lane == 0` branch with the descriptors built
-// on the way, an MMA costs 76-90 cycles whatever its size; here 32 (N = 64, A in TMEM), 48
-// (A in shared memory, bound by its 6 KB of operand reads) and 128 (N = 256), measured with all
-// SMs issuing.  A 64-key tile is then 20 x 32 + 16 x 48 + 4 x 128 = 1920 cycles of tensor pipe
-// at (576, 512).
+// Both CTAs gathering whole keys and computing all logits instead (nothing exchanged): 592 rows x
+// 2048 keys of (576, 512) take 408 us from the bf16 cache and 496 us from the 8-bit one, against 395
+// and 436 here.  There the shared-memory pipe is the limit (bf16 rows 98% busy: 36 KB of copies in
+// and 64 + 72 KB of MMA operands a tile out); here it is the chain of a tile's exchange and softmax,
+// some 4200 cycles with two tiles in flight.
+//
+// Tensor work of a tile at (576, 512): 16 or 20 QK MMAs of N = 64 (32 cycles each, A in TMEM) and
+// 4 PV MMAs of N = 256 (128 cycles): 1090 cycles on average of the some 1950 a tile takes.  The
+// MMAs are issued by one elected lane of a converged warp (elect.sync) from precomputed
+// descriptors: issued from an ordinary `lane == 0` branch with the descriptors built on the way,
+// one costs 76-90 cycles whatever its size.
 //
 // 8-bit rows: the gather warps read the codes into registers, expand them to bf16 (exactly: the
 // scales are powers of two) and store them into the same swizzled tiles the bf16 gather fills
 // with cp.async; the rotary dims are bf16 in both caches and always come by cp.async.
 //
-// Warp roles (512 threads): warp 0 issues the MMAs, warp 1 owns TMEM, warps 4-7 Q into TMEM, softmax and
-// epilogue (thread = head), warps 8-11 the K part and warps 12-15 the V part of every tile.
+// Warp roles (512 threads), q = warp % 4 being the TMEM lanes [32 q, 32 q + 32) a warp can reach
+// and q / 2 the CTA that owns those heads:
+//   warps 0-7 in the owner: the softmax of quarter q, warp < 4 the even tiles, the others the odd
+//   warp < 4, not the owner's: q even issues the QK products, q odd the PV products, each after
+//                rescaling O of its quarter when the owner moved a head's reference
+//   warps 4-7, not the owner's: send quarter q's partial logits away
+//   warps 8-15   resolve the keys, then gather (8 rows of every tile each)
 // Without idx the keys are every prior key; a 64-key tile is then one page, and the pages of a
 // split's tiles are resolved up front (kMaxDenseTiles of them).
 #pragma once
 #include "q8_row.cuh"
 #include "rows.cuh"
-#include "sparse_mla.cuh"
+#include "sm100.cuh"
 
 namespace dsa {
 
@@ -46,43 +60,6 @@ struct PagedMlaParams {
   int32_t* status;
 };
 
-// Rings of one CTA: the K part's value blocks in one slot (freed as soon as their MMAs have run,
-// refilled while the V part's run), the rotary block in two, the V part in three (a slot is held
-// until PV, and the next use needs it only when the third QK after comes to its V part).
-template <int D_QK, int D_V>
-struct PagedCfg {
-  static constexpr int KB_ALL = (D_QK + 63) / 64;     // 64-dim k-blocks of a latent row
-  static constexpr int V_HALF = D_V / 2;              // value dims per CTA
-  static constexpr int VKB = V_HALF / 64;             // value blocks per CTA (V part)
-  static constexpr int NK = KB_ALL - VKB - 1;         // value blocks of the other CTA (K part)
-  static constexpr int BN = 64;                       // keys per tile
-  static constexpr int R_SLOTS = 2, V_SLOTS = 3;
-  static constexpr int MAX_TILES = 32;                // topk <= 2048
-  static constexpr int THREADS = 512;
-  // TMEM: O, S, P (bf16), then the rotary and K-part blocks of Q and as many more as fit
-  static constexpr int S_COL = V_HALF;
-  static constexpr int P_COL = S_COL + BN;
-  static constexpr int Q_COL = P_COL + BN / 2;
-  static constexpr int KBT_MAX = (512 - Q_COL) / 32;
-  static constexpr int KBT = KB_ALL < KBT_MAX ? KB_ALL : KBT_MAX;   // Q blocks in TMEM
-  static constexpr int KBS = KB_ALL - KBT;                            // Q blocks in smem
-  static constexpr int TMEM_COLS = Q_COL + KBT * 32 <= 256 ? 256 : 512;
-  static constexpr int KB_BYTES = BN * 128;                           // one k-block of a tile
-  static constexpr int RING_BYTES = (NK + R_SLOTS + V_SLOTS * VKB) * KB_BYTES;
-  static constexpr int Q_KB_BYTES = 128 * 128;                        // one k-block of Q
-  static constexpr int Q_SMEM_BYTES = KBS * Q_KB_BYTES;
-  static constexpr int SMEM_USED = 1024 + Q_SMEM_BYTES + RING_BYTES + MAX_TILES * BN * 4 +
-                                   MAX_TILES * 12 + 256;
-  // at least 116 KB, so that one CTA runs per SM (its TMEM allocation never waits)
-  static constexpr int SMEM_BYTES = SMEM_USED > 116 * 1024 ? SMEM_USED : 116 * 1024;
-  static_assert(V_HALF % 64 == 0 && V_HALF <= 256, "PV MMA N");
-  static_assert(NK == VKB, "both parts hold as many value blocks");
-  static_assert(KBT >= NK + 1, "the K part's Q blocks live in TMEM");
-  static_assert(Q_COL + KBT * 32 <= 512, "TMEM columns");
-  static_assert(KBT * Q_KB_BYTES <= RING_BYTES, "Q staging fits the gather rings");
-  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-};
-
 constexpr int kMaxDenseTiles = 2048;   // tiles of one split without idx
 
 // True in one lane of the (converged) warp.
@@ -96,32 +73,105 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Whole-warp wait for phase `parity` of `bar`: every lane polls (one broadcast access) without a
-// suspend-time hint, which a completed phase answers in 14 cycles against 46 with the hint and 195
-// for warp_mbar_wait's poll by lane 0 and shuffle.  The clock and the abort flag are looked at
-// once in 64 polls; all lanes return the same result.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity,
-                                          const volatile int* abort) {
-  uint32_t ok = 0;
-  uint64_t t0 = 0;
-#pragma unroll 1
-  for (uint32_t it = 1;; ++it) {
+constexpr uint32_t kPollNs = 1000, kPolls = 1u << 22;   // see warp_wait
+
+// One poll of `bar` by every lane; kHint: the lanes may sleep until the phase completes (or
+// kPollNs).  kCluster: acquires what the other CTA of the cluster wrote before it arrived.
+template <bool kCluster, bool kHint>
+__device__ __forceinline__ uint32_t poll_bar(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (kHint && kCluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity), "r"(kPollNs) : "memory");
+  else if constexpr (kHint)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity), "r"(kPollNs) : "memory");
+  else if constexpr (kCluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  else
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) break;
-    if ((it & 63u) == 0) {
-      if (abort != nullptr && *abort) break;
-      const uint64_t now = global_timer_ns();
-      if (t0 == 0) t0 = now;
-      else if (now - t0 > kWaitLimitNs) break;
-    }
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok;
+}
+
+// Whole-warp wait for phase `parity` of `bar`; all lanes return the same result, false when the
+// wait gave up.  The first poll has no suspend-time hint, which a completed phase answers in 14
+// cycles (46 with the hint, 195 for a poll by lane 0 and a shuffle); the polls after it sleep up
+// to kPollNs, so that waiting warps leave the pipes to the others, and are kPolls at most: at
+// least 40 ms of 20-cycle polls, at most some 4 s of full sleeps.  The limit is a count, not a
+// clock, to keep the many inlined copies short: the kernel's loops compete for the instruction
+// caches.
+template <bool kCluster = false>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok = poll_bar<kCluster, false>(bar, parity);
+  if (!ok) {
+    uint32_t left = kPolls;
+#pragma unroll 1
+    do {
+      ok = poll_bar<kCluster, true>(bar, parity);
+    } while (!ok && --left != 0);
   }
   return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// Asynchronous stores into a CTA of the cluster (addr and bar are shared::cluster addresses of
+// that CTA); the bytes are counted on its barrier when they have landed.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                            uint32_t d, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, "
+      "[%5];" ::"r"(addr),
+      "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t addr, uint32_t a, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                   addr),
+               "r"(a), "r"(bar)
+               : "memory");
+}
+// Copies `bytes` of this CTA's shared memory into the same cluster's CTA that `dst` and `bar` lie in,
+// counted on its barrier when they have landed.
+__device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, uint32_t src, uint32_t bytes,
+                                                  uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst), "r"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+// Arrive on a barrier of another CTA of the cluster without releasing anything: it says that
+// values have been read (and are in registers), not that something was written.  The releasing
+// form waits for this thread's stores to reach the other SM first, 500 cycles and more.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Arrive once on the barrier at this offset in every CTA of `mask` when every tcgen05 operation
+// this thread issued so far has completed.
+__device__ __forceinline__ void umma_commit_multicast(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"(mask)
+      : "memory");
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 
 // 2^x, results below the normal range flushed to 0 (a probability that small adds nothing).
@@ -131,47 +181,104 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// Grid: x = 2 * row + v, y = split.  Tile sizes, rings and TMEM columns are MlaCfg's.
+// Tile sizes, rings and columns.
+template <int D_QK, int D_V>
+struct PagedCfg {
+  static constexpr int KB_ALL = (D_QK + 63) / 64;     // 64-dim k-blocks of a latent row
+  static constexpr int V_HALF = D_V / 2;              // value dims per CTA
+  static constexpr int VKB = V_HALF / 64;             // value blocks per CTA
+  static constexpr int BN = 64;                       // keys per tile
+  static constexpr int V_SLOTS = 5;                   // a slot is held from QK to PV, some 3 tiles
+  static constexpr int MAX_TILES = 32;                // topk <= 2048
+  static constexpr int THREADS = 512;
+  static constexpr int GATHER = 256;                  // gathering threads
+  // TMEM: O, S, the rotary block of Q, the CTA's value blocks of Q
+  static constexpr int S_COL = V_HALF;
+  static constexpr int QR_COL = S_COL + BN;
+  static constexpr int Q_COL = QR_COL + 32;
+  static constexpr int TMEM_USED = Q_COL + VKB * 32;
+  static constexpr int TMEM_COLS = TMEM_USED <= 256 ? 256 : 512;
+  static constexpr int KB_BYTES = BN * 128;           // one k-block of a tile
+  static constexpr int V_SLOT_BYTES = VKB * KB_BYTES;
+  static constexpr int Q_KB_BYTES = 128 * 128;        // one k-block of Q
+  static constexpr int P_BYTES = 128 * 128;           // 128 heads x 64 keys bf16, twice
+  static constexpr int X_BYTES = BN * 64 * 4;         // partial logits of 64 heads
+  static constexpr int P_TX = 64 * 128 + 64 * 4;      // the partner's probabilities and rescales
+  // (the dynamic array starts on a 1024-byte boundary: the kernel has no static shared memory)
+  static constexpr int BARS = 39;
+  static constexpr int SMEM_USED = V_SLOTS * V_SLOT_BYTES + KB_BYTES + 2 * P_BYTES + X_BYTES +
+                                   MAX_TILES * BN * 4 + MAX_TILES * 12 + 4 * 64 * 4 + BARS * 8;
+  // at least 116 KB, so that one CTA runs per SM (its TMEM allocation never waits)
+  static constexpr int SMEM_BYTES = SMEM_USED > 116 * 1024 ? SMEM_USED : 116 * 1024;
+  static_assert(V_HALF % 64 == 0 && V_HALF <= 256, "PV MMA N");
+  static_assert(2 * VKB + 1 == KB_ALL, "value blocks and one rotary block");
+  static_assert(TMEM_USED <= 512, "TMEM columns");
+  static_assert((VKB + 1) * Q_KB_BYTES <= V_SLOTS * V_SLOT_BYTES, "Q staging fits the ring");
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+};
+
+// Multiplies COLS columns of O (this warp's lanes) by alpha.
+template <int COLS>
+__device__ __forceinline__ void rescale_o(uint32_t addr, float alpha) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < COLS; c0 += 32) {
+    uint32_t u[32];
+    tmem_ld32(addr + c0, u);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * alpha);
+    tmem_st32(addr + c0, u);
+  }
+  tmem_wait_st();
+}
+
+// Grid: x = 2 * row + c (clusters of two), y = split.
 template <int D_QK, int D_V, bool kQ8>
 __global__ void __launch_bounds__(512, 1)
     dsa_paged_mla_kernel(const __grid_constant__ CUtensorMap q_map, const PagedMlaParams p) {
   using C = PagedCfg<D_QK, D_V>;
   using R = Q8Row<D_QK, D_V>;
   constexpr int ROW_BYTES = kQ8 ? R::BYTES : D_QK * 2;
-  static_assert(R::ROPE <= 64 && D_V % 64 == 0, "rotary dims fill (part of) the last k-block");
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  uint8_t* sQ = smem;                                           // [KBS][128 heads][128 B]
-  uint8_t* sRing = sQ + C::Q_SMEM_BYTES;                        // gather rings (Q staging first)
-  uint8_t* sK = sRing;                                          // [NK k-blocks]
-  uint8_t* sR = sK + C::NK * C::KB_BYTES;                       // [R_SLOTS] rotary k-blocks
-  uint8_t* sV = sR + C::R_SLOTS * C::KB_BYTES;                  // [V_SLOTS][VKB k-blocks]
+  static_assert(R::ROPE <= 64 && D_V % 128 == 0, "rotary dims fill (part of) the last k-block");
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sV = smem;                                           // [V_SLOTS] (Q staging first)
+  uint8_t* sR = sV + C::V_SLOTS * C::V_SLOT_BYTES;              // rotary block of a tile
+  uint8_t* sP = sR + C::KB_BYTES;                               // [2] probabilities, all heads
+  uint8_t* sX = sP + 2 * C::P_BYTES;   // [16 key quads][64 heads][4]: the partner's half logits
   // selected: the physical row of every key; dense: the first physical row of every tile
-  int32_t* sPhys = reinterpret_cast<int32_t*>(sRing + C::RING_BYTES);             // [2048]
+  int32_t* sPhys = reinterpret_cast<int32_t*>(sX + C::X_BYTES);                   // [2048]
   uint64_t* sMask = reinterpret_cast<uint64_t*>(sPhys + C::MAX_TILES * C::BN);   // [32]
   int32_t* sTiles = reinterpret_cast<int32_t*>(sMask + C::MAX_TILES);            // [32]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sTiles + C::MAX_TILES);
-  uint64_t* k_full = bars;           // every K-part thread
-  uint64_t* k_empty = bars + 1;      // commit of the K part's MMAs
-  uint64_t* r_full = bars + 2;       // [2] every K-part thread (rotary copies landed)
-  uint64_t* r_empty = bars + 4;      // [2] the same commit
-  uint64_t* v_full = bars + 6;       // [3] every V-part thread
-  uint64_t* v_empty = bars + 9;      // [3] PV commit
-  uint64_t* s_full = bars + 12;       // QK commit
-  uint64_t* s_empty = bars + 13;      // 4 softmax warps
-  uint64_t* p_full = bars + 14;      // 4 softmax warps
-  uint64_t* pv_done = bars + 15;     // PV commit
-  uint64_t* mma_fin = bars + 16;     // every MMA of this CTA completed
-  uint64_t* q_bar = bars + 17;       // 1 arrival + Q bytes
-  __shared__ uint32_t tmem_base_s;
-  __shared__ int abort_s;
-  __shared__ int n_act_s;
+  float* sAlpha = reinterpret_cast<float*>(sTiles + C::MAX_TILES);   // [2][64] from the partner
+  float* sRef = sAlpha + 2 * 64;                  // [2][64 heads] the reference after a tile
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sRef + 2 * 64);
+  // after the last tile, over the rows that no one reads any more:
+  float* sSum = reinterpret_cast<float*>(sPhys);  // [2 warps][sum, reference][64 heads]
+  float* sInv = sSum + 4 * 64;                    // [128] 1 / sum
+  uint64_t* v_full = bars;           // [5] every gathering thread
+  uint64_t* v_empty = bars + 5;      // [5] PV commit
+  uint64_t* r_full = bars + 10;      // every gathering thread (rotary copies landed)
+  uint64_t* r_empty = bars + 11;     // QK commit of a rotary tile
+  uint64_t* s_full = bars + 12;      // [2 tiles] QK commit
+  uint64_t* s_empty = bars + 14;     // the 2 softmax warps of the tile and the 2 senders
+  uint64_t* x_full = bars + 15;      // [2 tiles][2 key halves] a local arrival + the partner's bytes
+  uint64_t* x_free = bars + 19;      // [2 key halves] the partner's 2 softmax warps have read it
+  uint64_t* p_full = bars + 21;      // [2] 2 local softmax warps + P_TX bytes from the partner
+  uint64_t* p_empty = bars + 23;     // [2] both CTAs' PV commits
+  uint64_t* o_ok = bars + 25;        // [2] the QK issuer has rescaled its quarter of O
+  uint64_t* pv_done = bars + 27;     // [2] PV commit
+  uint64_t* m_full = bars + 29;      // [2 quarters][2] the reference after a tile is in sRef
+  uint64_t* mma_fin = bars + 33;     // [2] every MMA of an issuer completed
+  uint64_t* q_bar = bars + 35;       // 1 arrival + Q bytes
+  volatile uint32_t& tmem_base_s = *reinterpret_cast<volatile uint32_t*>(bars + 36);
+  volatile int& abort_s = *reinterpret_cast<volatile int*>(bars + 37);
+  volatile int& n_act_s = *reinterpret_cast<volatile int*>(bars + 38);
   static_assert(kMaxDenseTiles <= C::MAX_TILES * C::BN, "dense tiles fit the key array");
 
   wait_prior_grid();   // (launched early: the indices come from the previous kernel)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int vh = static_cast<int>(blockIdx.x & 1u);   // value half
+  const int c = static_cast<int>(cluster_ctarank());   // value half, and the heads it owns
+  const uint32_t peer = static_cast<uint32_t>(c ^ 1);
   const int split = blockIdx.y;
   const int r = blockIdx.x >> 1;
   const int row = p.row_begin + r;
@@ -197,41 +304,42 @@ __global__ void __launch_bounds__(512, 1)
   if (bad_row && threadIdx.x == 0 && p.status) atomicOr(p.status, kStatusBadIndex);
 
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(k_full), 128);
-    mbar_init(smem_u32(k_empty), 1);
-    for (int i = 0; i < C::R_SLOTS; ++i) {
-      mbar_init(smem_u32(&r_full[i]), 128);
-      mbar_init(smem_u32(&r_empty[i]), 1);
-    }
     for (int i = 0; i < C::V_SLOTS; ++i) {
-      mbar_init(smem_u32(&v_full[i]), 128);
+      mbar_init(smem_u32(&v_full[i]), C::GATHER);
       mbar_init(smem_u32(&v_empty[i]), 1);
     }
-    mbar_init(smem_u32(s_full), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&x_free[i]), 2);
+      mbar_init(smem_u32(&p_full[i]), 2);
+      mbar_init(smem_u32(&p_empty[i]), 2);
+      mbar_init(smem_u32(&o_ok[i]), 1);
+      mbar_init(smem_u32(&pv_done[i]), 1);
+      mbar_init(smem_u32(&mma_fin[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&x_full[i]), 1);
+      mbar_init(smem_u32(&m_full[i]), 1);
+    }
+    mbar_init(smem_u32(r_full), C::GATHER);
+    mbar_init(smem_u32(r_empty), 1);
+    mbar_init(smem_u32(&s_full[0]), 1);
+    mbar_init(smem_u32(&s_full[1]), 1);
     mbar_init(smem_u32(s_empty), 4);
-    mbar_init(smem_u32(p_full), 4);
-    mbar_init(smem_u32(pv_done), 1);
-    mbar_init(smem_u32(mma_fin), 1);
     mbar_init(smem_u32(q_bar), 1);
     abort_s = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(smem_u32(&tmem_base_s), C::TMEM_COLS);
+  if (warp == 1) tmem_alloc(smem_u32(bars + 36), C::TMEM_COLS);
   __syncthreads();
   if (threadIdx.x == 0) {
-    // ---- Q, in the order rotary, K part, V part: KBT blocks into the (still idle) rings, the rest
-    // into sQ; h rows a block (lanes past h hold whatever the staging area held and are never written)
+    // ---- Q: the rotary block and the CTA's value blocks into the (still idle) ring, h rows a block
+    // (lanes past h hold whatever was there and are never written out)
     const uint32_t kb_bytes = static_cast<uint32_t>(p.h) * 128u;
     tma_prefetch_desc(&q_map);
-    mbar_arrive_expect_tx(smem_u32(q_bar), C::KB_ALL * kb_bytes);
-    for (int j = 0; j < C::KB_ALL; ++j) {
-      const int v0 = vh * C::VKB;
-      const int kb = j == 0 ? C::KB_ALL - 1
-                   : j > C::NK ? v0 + j - 1 - C::NK
-                               : (j - 1 < v0 ? j - 1 : j - 1 + C::VKB);
-      uint8_t* dst = j < C::KBT ? sRing + j * C::Q_KB_BYTES : sQ + (j - C::KBT) * C::Q_KB_BYTES;
-      tma_load_2d(smem_u32(dst), &q_map, smem_u32(q_bar), kb * 128, r * p.h);
-    }
+    mbar_arrive_expect_tx(smem_u32(q_bar), (C::VKB + 1) * kb_bytes);
+    for (int j = 0; j <= C::VKB; ++j)
+      tma_load_2d(smem_u32(sV + j * C::Q_KB_BYTES), &q_map, smem_u32(q_bar),
+                  (j == 0 ? C::KB_ALL - 1 : c * C::VKB + j - 1) * 128, r * p.h);
   }
   bool bad_idx = false;
   if (warp >= 8 && !dense) {
@@ -314,17 +422,16 @@ __global__ void __launch_bounds__(512, 1)
     n_act_s = t1 - t0;
   }
   if (warp >= 4 && warp < 8) {
-    // ---- Q blocks [0, KBT) from the staging area into TMEM: head = lane, dim d in column
-    // Q_COL + d / 2
+    // ---- Q from the staging area into TMEM: head = lane, two dims a column
     const int hrow = (warp & 3) * 32 + lane;
     const uint32_t lane_addr = tmem_base_s + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    if (!(warp_wait(smem_u32(q_bar), 0, &abort_s))) {
+    if (!(warp_wait(smem_u32(q_bar), 0))) {
       abort_s = 1;
       if (p.status) atomicOr(p.status, kStatusTimeout);
     } else {
-      for (int kb = 0; kb < C::KBT; ++kb) {
+      for (int kb = 0; kb <= C::VKB; ++kb) {
         uint32_t u[32];
-        const uint8_t* src = sRing + kb * C::Q_KB_BYTES;
+        const uint8_t* src = sV + kb * C::Q_KB_BYTES;
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) {
           const uint4 q4 = *reinterpret_cast<const uint4*>(src + sw128_offset(hrow, ch));
@@ -333,13 +440,14 @@ __global__ void __launch_bounds__(512, 1)
           u[4 * ch + 2] = q4.z;
           u[4 * ch + 3] = q4.w;
         }
-        tmem_st32(lane_addr + C::Q_COL + kb * 32, u);
+        tmem_st32(lane_addr + C::QR_COL + kb * 32, u);
       }
       tmem_wait_st();
     }
   }
   tc_fence_before();
-  __syncthreads();   // the staging area is free for the gather rings from here on
+  __syncwarp();
+  cluster_sync();   // the staging area is free for the ring, both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
   const int n = abort_s ? 0 : n_act_s;
@@ -354,80 +462,61 @@ __global__ void __launch_bounds__(512, 1)
     return ((mask_of(i) >> rr) & 1ull) ? base + rr : base;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ MMA issuer
-    // QK(i) is issued before PV(i - 1), so that the tensor pipe runs PV(i - 1) while the softmax
-    // warps read S(i) out of its single buffer (and QK(i + 1) still has to wait for them).
-    constexpr uint32_t idesc_qk = idesc_f32acc(1 /* bf16 */, 128, C::BN, 0, 0);
-    constexpr uint32_t idesc_pv = idesc_f32acc(1, 128, C::V_HALF, 0, 1);
-    const uint64_t qd = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    bool ok = n == 0 || warp_wait(smem_u32(q_bar), 0, &abort_s);
-    const uint64_t kd = sdesc_sw128(smem_u32(sK), 16, 1024);
-    int vs = 0, vs1 = 0;            // V slots of tiles i and i - 1
+  const int q = warp & 3;                          // TMEM lane quarter of this warp
+  const bool own = (q >> 1) == c;                  // whose heads this CTA owns
+  // O of a quarter the partner owns, to the references of tile j (this warp's lanes)
+  auto fix_o = [&](int j) -> bool {
+    const float alpha = sAlpha[(j & 1) * 64 + (q & 1) * 32 + lane];
+    if (j < 1 || !__any_sync(0xffffffffu, alpha != 1.f)) return true;
+    if (!warp_wait(smem_u32(&pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1)) return false;
+    tc_fence_after();
+    rescale_o<C::V_HALF>(tmem + (static_cast<uint32_t>(q * 32) << 16), alpha);
+    tc_fence_before();
+    return true;
+  };
+  if (warp < 4 && !own && (q & 1) == 0) {
+    // ------------------------------------------------------------ QK issuer
+    constexpr uint32_t idesc = idesc_f32acc(1 /* bf16 */, 128, C::BN, 0, 0);
+    const uint64_t rd = sdesc_sw128(smem_u32(sR), 16, 1024);
+    const uint32_t d = tmem + C::S_COL;
+    bool ok = true;
+    int vs = 0;
     uint32_t vph = 0;
-    for (int i = 0; i <= n && ok; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < n + 2 && ok; ++i) {
       if (i < n) {
-        const int rs = i & 1;
-        const uint64_t rd = sdesc_sw128(smem_u32(sR + rs * C::KB_BYTES), 16, 1024);
-        const uint64_t vd = sdesc_sw128(smem_u32(sV + vs * (C::VKB * C::KB_BYTES)), 16, 1024);
-        ok = warp_wait(smem_u32(&r_full[rs]), (i >> 1) & 1, &abort_s) &&
-             warp_wait(smem_u32(k_full), i & 1, &abort_s) &&
-             (i == 0 || warp_wait(smem_u32(s_empty), (i - 1) & 1, &abort_s));
+        const bool rot = (i & 1) == c;               // this CTA adds the tile's rotary dims
+        const uint64_t vd = sdesc_sw128(smem_u32(sV + vs * C::V_SLOT_BYTES), 16, 1024);
+        ok = warp_wait(smem_u32(&v_full[vs]), vph) &&
+             (!rot || warp_wait(smem_u32(r_full), (i >> 1) & 1)) &&
+             (i < 1 || warp_wait(smem_u32(s_empty), (i - 1) & 1));
         if (!ok) break;
         tc_fence_after();
         fence_proxy_async_smem();   // the rows were written by cp.async and ordinary stores
         if (elect_one()) {
+          if (rot) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_bf16_ts(tmem + C::S_COL, tmem + C::Q_COL + k * 8, rd + k * 2, idesc_qk, k != 0);
-#pragma unroll
-          for (int k = 0; k < 4 * C::NK; ++k)
-            umma_bf16_ts(tmem + C::S_COL, tmem + C::Q_COL + 32 + k * 8,
-                         kd + ((k / 4) * C::KB_BYTES + (k % 4) * 32) / 16, idesc_qk, 1u);
-          umma_commit(smem_u32(k_empty));
-          umma_commit(smem_u32(&r_empty[rs]));
-        }
-        __syncwarp();
-        ok = warp_wait(smem_u32(&v_full[vs]), vph, &abort_s);
-        if (!ok) break;
-        tc_fence_after();
-        fence_proxy_async_smem();
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 4 * C::VKB; ++k) {
-            const int j = 1 + C::NK + k / 4;         // Q block
-            const uint64_t bd = vd + ((k / 4) * C::KB_BYTES + (k % 4) * 32) / 16;
-            if (j < C::KBT)
-              umma_bf16_ts(tmem + C::S_COL, tmem + C::Q_COL + j * 32 + (k % 4) * 8, bd, idesc_qk,
-                           1u);
-            else
-              umma_bf16(tmem + C::S_COL,
-                        qd + ((j - C::KBT) * C::Q_KB_BYTES + (k % 4) * 32) / 16, bd, idesc_qk, 1u);
+            for (int k = 0; k < 4; ++k)
+              umma_bf16_ts(d, tmem + C::QR_COL + k * 8, rd + k * 2, idesc, k != 0);
+            umma_commit(smem_u32(r_empty));
           }
-          umma_commit(smem_u32(s_full));
-        }
-        __syncwarp();
-      }
-      if (i > 0) {
-        const uint64_t vd = sdesc_sw128(smem_u32(sV + vs1 * (C::VKB * C::KB_BYTES)), C::KB_BYTES,
-                                        1024);
-        ok = warp_wait(smem_u32(p_full), (i - 1) & 1, &abort_s);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < C::BN / 16; ++k)
-            umma_bf16_ts(tmem, tmem + C::P_COL + k * 8, vd + k * 16 * 128 / 16, idesc_pv,
-                         i > 1 || k != 0);
-          umma_commit(smem_u32(&v_empty[vs1]));
-          umma_commit(smem_u32(pv_done));
+          for (int k = 0; k < 4 * C::VKB; ++k)
+            umma_bf16_ts(d, tmem + C::Q_COL + k * 8,
+                         vd + ((k / 4) * C::KB_BYTES + (k % 4) * 32) / 16, idesc, rot || k != 0);
+          umma_commit(smem_u32(&s_full[i & 1]));
         }
         __syncwarp();
+        if (++vs == C::V_SLOTS) {
+          vs = 0;
+          vph ^= 1u;
+        }
       }
-      vs1 = vs;
-      if (++vs == C::V_SLOTS) {
-        vs = 0;
-        vph ^= 1u;
+      if (i >= 2) {                                  // O of this quarter for PV(i - 2)
+        const int j = i - 2;
+        ok = warp_wait<true>(smem_u32(&p_full[j & 1]), (j >> 1) & 1) && fix_o(j);
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(smem_u32(&o_ok[j & 1]));
       }
     }
     if (!ok) {
@@ -435,247 +524,378 @@ __global__ void __launch_bounds__(512, 1)
       if (lane == 0 && p.status) atomicOr(p.status, kStatusTimeout);
     }
     __syncwarp();
-    if (elect_one()) umma_commit(smem_u32(mma_fin));   // no MMA may outlive the CTA
+    if (elect_one()) umma_commit(smem_u32(&mma_fin[0]));   // no MMA may outlive the CTA
     __syncwarp();
-    warp_wait(smem_u32(mma_fin), 0, nullptr);
+    warp_wait(smem_u32(&mma_fin[0]), 0);
+  } else if (warp < 4 && !own) {
+    // ------------------------------------------------------------ PV issuer
+    constexpr uint32_t idesc = idesc_f32acc(1, 128, C::V_HALF, 0, 1);
+    bool ok = true;
+    int vs = 0;
+#pragma unroll 1
+    for (int j = 0; j < n && ok; ++j) {
+      const int b2 = j & 1;
+      const uint64_t vd = sdesc_sw128(smem_u32(sV + vs * C::V_SLOT_BYTES), C::KB_BYTES, 1024);
+      const uint64_t pd = sdesc_sw128(smem_u32(sP + b2 * C::P_BYTES), 16, 1024);
+      ok = warp_wait<true>(smem_u32(&p_full[b2]), (j >> 1) & 1) && fix_o(j) &&
+           warp_wait(smem_u32(&o_ok[b2]), (j >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      fence_proxy_async_smem();   // P was written by ordinary stores and by the partner's copy
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < C::BN / 16; ++k)
+          umma_bf16(tmem, pd + k * 2, vd + k * 16 * 128 / 16, idesc, j > 0 || k != 0);
+        umma_commit(smem_u32(&v_empty[vs]));
+        umma_commit(smem_u32(&pv_done[b2]));
+        umma_commit_multicast(smem_u32(&p_empty[b2]), 3);
+      }
+      __syncwarp();
+      if (++vs == C::V_SLOTS) vs = 0;
+    }
+    if (!ok) {
+      abort_s = 1;
+      if (lane == 0 && p.status) atomicOr(p.status, kStatusTimeout);
+    }
+    __syncwarp();
+    if (elect_one()) umma_commit(smem_u32(&mma_fin[1]));
+    __syncwarp();
+    warp_wait(smem_u32(&mma_fin[1]), 0);
   } else if (warp >= 8) {
-    // ------------------------------------------------------------ gather producers
-    // Warp 8 + 4 part + w fills rows [16w, 16w + 16) of each tile: part 0 the K part (and the
-    // rotary block), part 1 the V part.
-    const int part = (warp - 8) >> 2;
-    const int pw = (warp - 8) & 3;
+    // ------------------------------------------------------------ gather
+    // warp 8 + pw fills rows [8 pw, 8 pw + 8) of each tile
+    const int pw = warp - 8;
     const int ch = lane & 7;                    // 16-byte chunk of a 128-byte row block
-    const int rsub = lane >> 3;                 // rows rsub, rsub + 4, rsub + 8, rsub + 12
-    const int kb0 = (part == 0) == (vh == 0) ? C::VKB : 0;   // the part's first latent block
+    const int rsub = lane >> 3;                 // rows rsub, rsub + 4
+    const int kb0 = c * C::VKB;                 // the CTA's first latent block
+    // Physical rows, one tile ahead: lane l holds that of row 8 pw + l % 8, the others come by
+    // shuffle, so that no copy waits for a chain of shared-memory loads.
+    auto rows_of = [&](int i) { return static_cast<int32_t>(phys_of(i, pw * 8 + (lane & 7))); };
+    auto row_ptr = [&](int32_t rows, int l) {
+      return p.kv + static_cast<int64_t>(__shfl_sync(0xffffffffu, rows, l)) * ROW_BYTES;
+    };
     // a block of bf16 rows straight from the cache, its chunks past `valid` zeros
-    auto copy_block = [&](uint8_t* dst, int i, int byte, int valid) {
+    auto copy_block = [&](uint8_t* dst, const uint8_t* const (&src)[2], int byte, int valid) {
       const bool in = ch < valid;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int rr = pw * 16 + rsub + 4 * j;
-        const uint8_t* src = p.kv + phys_of(i, rr) * ROW_BYTES + byte + ch * 16;
-        cp_async_16(smem_u32(dst) + sw128_offset(rr, ch), in ? src : p.kv, in ? 16u : 0u);
-      }
+      for (int j = 0; j < 2; ++j)
+        cp_async_16(smem_u32(dst) + sw128_offset(pw * 8 + rsub + 4 * j, ch),
+                    in ? src[j] + byte + ch * 16 : p.kv, in ? 16u : 0u);
     };
-    // 8-bit codes: lane = 16-code chunk lane % 4 of rows lane / 4 and lane / 4 + 8, every value block
-    // of the part.  Eight lanes, two neighbouring rows, then store to the eight different 16-byte
-    // columns of a swizzled tile (eight lanes on one row would meet two to a column: 8.1 instead
-    // of 4 wavefronts a store).  Two register sets take turns: the set just stored is loaded with
-    // the codes and scales of two tiles on, so that their latency (HBM's, where the cache is
-    // large) goes by under a whole tile.
-    constexpr int GP = (C::VKB + 1) / 2;         // scales of a row's part (128 values, 2 blocks)
+    // 8-bit codes: lane = 16-code chunk lane % 4 of row lane / 4, every value block of the CTA.  Eight
+    // lanes, two neighbouring rows, then store to the eight different 16-byte columns of a swizzled
+    // tile (eight lanes on one row would meet two to a column: 8.1 instead of 4 wavefronts a
+    // store).  Two register sets take turns: the set just stored is loaded with the codes and
+    // scales of two tiles on, so that their latency goes by under a whole tile.
+    constexpr int GP = (C::VKB + 1) / 2;         // scales of a row's half (128 values, 2 blocks)
     struct CodeSet {
-      uint4 code[2][C::VKB];
-      float scale[2][GP];
+      uint4 code[C::VKB];
+      float scale[GP];
     };
-    const int cl = lane & 3, rl = pw * 16 + (lane >> 2);
-    auto load_set = [&](CodeSet& x, int i) {
+    const int cl = lane & 3, rl = pw * 8 + (lane >> 2);
+    auto load_set = [&](CodeSet& x, int32_t rows) {
+      const uint8_t* src = row_ptr(rows, lane >> 2);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const uint8_t* src = p.kv + phys_of(i, rl + 8 * q) * ROW_BYTES;
+      for (int g = 0; g < GP; ++g)
+        x.scale[g] = __ldg(reinterpret_cast<const float*>(src + R::SCALE_OFF) + kb0 / 2 + g);
 #pragma unroll
-        for (int g = 0; g < GP; ++g)
-          x.scale[q][g] = __ldg(reinterpret_cast<const float*>(src + R::SCALE_OFF) + kb0 / 2 + g);
-#pragma unroll
-        for (int ks = 0; ks < C::VKB; ++ks)
-          x.code[q][ks] = __ldg(reinterpret_cast<const uint4*>(src + (kb0 + ks) * 64) + cl);
-      }
+      for (int ks = 0; ks < C::VKB; ++ks)
+        x.code[ks] = __ldg(reinterpret_cast<const uint4*>(src + (kb0 + ks) * 64) + cl);
     };
     auto store_set = [&](const CodeSet& x, uint8_t* dst) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int ks = 0; ks < C::VKB; ++ks) {
-          uint8_t* at = dst + ks * C::KB_BYTES;
-          uint4 lo, hi;
-          q8_expand16(x.code[q][ks], x.scale[q][ks / 2], lo, hi);
-          *reinterpret_cast<uint4*>(at + sw128_offset(rl + 8 * q, 2 * cl)) = lo;
-          *reinterpret_cast<uint4*>(at + sw128_offset(rl + 8 * q, 2 * cl + 1)) = hi;
-        }
+      for (int ks = 0; ks < C::VKB; ++ks) {
+        uint8_t* at = dst + ks * C::KB_BYTES;
+        uint4 lo, hi;
+        q8_expand16(x.code[ks], x.scale[ks / 2], lo, hi);
+        *reinterpret_cast<uint4*>(at + sw128_offset(rl, 2 * cl)) = lo;
+        *reinterpret_cast<uint4*>(at + sw128_offset(rl, 2 * cl + 1)) = hi;
+      }
     };
     bool ok = true;
     int vs = 0;
     uint32_t vph = 1;                            // (the first use of each slot does not wait)
-    // tile i: its slot waited for, filled, and the barrier told
-    auto fill = [&](CodeSet& x, int i) -> bool {
-      uint8_t* dst;
-      uint64_t* full;
-      if (part == 0) {
-        const int rs = i & 1;
-        if (i >= C::R_SLOTS &&
-            !warp_wait(smem_u32(&r_empty[rs]), ((i >> 1) - 1) & 1, &abort_s))
-          return false;
-        copy_block(sR + rs * C::KB_BYTES, i, kQ8 ? R::ROPE_OFF : 2 * D_V, R::ROPE / 8);
-        cp_async_arrive_noinc(smem_u32(&r_full[rs]));
-        if (i >= 1 && !warp_wait(smem_u32(k_empty), (i - 1) & 1, &abort_s)) return false;
-        dst = sK;
-        full = k_full;
-      } else {
-        if (i >= C::V_SLOTS && !warp_wait(smem_u32(&v_empty[vs]), vph, &abort_s)) return false;
-        dst = sV + vs * (C::VKB * C::KB_BYTES);
-        full = &v_full[vs];
-        if (++vs == C::V_SLOTS) {
-          vs = 0;
-          vph ^= 1u;
-        }
+    // tile i (physical rows `rows`): its slots waited for, filled, and the barriers told; the set x
+    // is then loaded with tile i + 2 (rows `rows2`)
+    auto fill = [&](CodeSet& x, int i, int32_t rows, int32_t rows2) -> bool {
+      const uint8_t* const src[2] = {row_ptr(rows, rsub), row_ptr(rows, rsub + 4)};
+      if ((i & 1) == c) {                        // the rotary block, on this CTA's tiles
+        if (i >= 2 && !warp_wait(smem_u32(r_empty), ((i >> 1) - 1) & 1)) return false;
+        copy_block(sR, src, kQ8 ? R::ROPE_OFF : 2 * D_V, R::ROPE / 8);
+        cp_async_arrive_noinc(smem_u32(r_full));
+      }
+      if (i >= C::V_SLOTS && !warp_wait(smem_u32(&v_empty[vs]), vph)) return false;
+      uint8_t* dst = sV + vs * C::V_SLOT_BYTES;
+      uint64_t* full = &v_full[vs];
+      if (++vs == C::V_SLOTS) {
+        vs = 0;
+        vph ^= 1u;
       }
       if constexpr (kQ8) {
         store_set(x, dst);
         fence_proxy_async_smem();              // this thread's stores, before the MMAs read them
         mbar_arrive(smem_u32(full));
-        if (i + 2 < n) load_set(x, i + 2);
+        if (i + 2 < n) load_set(x, rows2);
       } else {
 #pragma unroll
         for (int ks = 0; ks < C::VKB; ++ks)
-          copy_block(dst + ks * C::KB_BYTES, i, (kb0 + ks) * 128, 8);
+          copy_block(dst + ks * C::KB_BYTES, src, (kb0 + ks) * 128, 8);
         cp_async_arrive_noinc(smem_u32(full));
       }
       return true;
     };
     CodeSet set0, set1;
+    int32_t rows0 = n > 0 ? rows_of(0) : 0, rows1 = n > 1 ? rows_of(1) : 0;
     if constexpr (kQ8) {
-      if (n > 0) load_set(set0, 0);
-      if (n > 1) load_set(set1, 1);
+      if (n > 0) load_set(set0, rows0);
+      if (n > 1) load_set(set1, rows1);
     }
-    for (int i = 0; i < n && ok; i += 2) {
-      ok = fill(set0, i);
-      if (ok && i + 1 < n) ok = fill(set1, i + 1);
+#pragma unroll 1
+    for (int i = 0; i < n && ok; i += 2) {       // (the sets by name: a copy would wait for its loads)
+      const int32_t rows2 = i + 2 < n ? rows_of(i + 2) : 0, rows3 = i + 3 < n ? rows_of(i + 3) : 0;
+      ok = fill(set0, i, rows0, rows2);
+      if (ok && i + 1 < n) ok = fill(set1, i + 1, rows1, rows3);
+      rows0 = rows2;
+      rows1 = rows3;
     }
     if (!ok) {
       abort_s = 1;
       if (p.status) atomicOr(p.status, kStatusTimeout);
     }
     cp_async_wait_all();   // nothing may still be writing this CTA's shared memory at exit
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------ softmax + epilogue
-    const int hrow = (warp & 3) * 32 + lane;    // head = TMEM lane
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    float m_ref = -INFINITY, l_sum = 0.f;
-    bool ok = !abort_s;
+  } else if (!own) {
+    // ------------------------------------------------------------ partial logits to their owner
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) + C::S_COL;
+    const uint32_t dst = map_to_rank(smem_u32(sX), peer) + ((q & 1) * 32 + lane) * 16;
+    const uint32_t bar = map_to_rank(smem_u32(x_full), peer);
+    bool ok = true;
+#pragma unroll 1
     for (int i = 0; i < n && ok; ++i) {
-      ok = (warp_wait(smem_u32(s_full), i & 1, &abort_s));
+      ok = warp_wait(smem_u32(&s_full[i & 1]), (i >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      uint32_t su[2][32];                       // S of keys [32 hh, 32 hh + 32)
-      tmem_ld32(lane_addr + C::S_COL, su[0]);
-      tmem_ld32(lane_addr + C::S_COL + 32, su[1]);
+      uint32_t su[2][32];
+      tmem_ld32(lane_addr, su[0]);
+      tmem_ld32(lane_addr + 32, su[1]);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(s_empty));
-      const uint64_t vmask = mask_of(i);
-      if (vmask != ~0ull) {
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const uint32_t vb = static_cast<uint32_t>(vmask >> (32 * hh));
-#pragma unroll
-          for (int j = 0; j < 32; ++j)           // invalid keys: -inf, so p = 0 below
-            if (!((vb >> j) & 1u)) su[hh][j] = 0xFF800000u;
-        }
-      }
-      // the tile max of the unscaled logits (sigma log2 e > 0), as 8 independent partial maxima
-      float mm[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) mm[q] = __uint_as_float(su[0][q]);
-#pragma unroll
-      for (int j = 8; j < 64; j += 16)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float x = __uint_as_float(su[(j + q) / 32][(j + q) % 32]);
-          const int j2 = j + 8 + q;
-          mm[q] = j2 < 64 ? fmaxf(fmaxf(mm[q], x), __uint_as_float(su[j2 / 32][j2 % 32]))
-                          : fmaxf(mm[q], x);
-        }
-      const float m_tile =
-          fmaxf(fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])),
-                fmaxf(fmaxf(mm[4], mm[5]), fmaxf(mm[6], mm[7]))) * p.scale_log2;
-      // the reference moves only when a tile beats it by 2^8: p and the sums stay far inside
-      // fp32 (and bf16) either way
-      const bool need = m_tile > m_ref + 8.0f;
-      float alpha = 1.f;
-      if (need) {
-        alpha = exp2_approx(m_ref - m_tile);
-        l_sum *= alpha;
-        m_ref = m_tile;
-      }
-      // p = 2^(sigma log2e s - m_ref); the denominator sums the fp32 probabilities, only the PV
-      // operand is rounded (bf16: the MMA's operand type)
-      // (two keys to an instruction: the scaling FMA and the sums are packed fp32 pairs)
-      float2 rs[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) rs[q] = make_float2(0.f, 0.f);
-      const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-m_ref, -m_ref);
-      uint32_t pk[2][16];
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 x = __ffma2_rn(make_float2(__uint_as_float(su[hh][2 * e]),
-                                                  __uint_as_float(su[hh][2 * e + 1])), sc2, nm2);
-          const float2 pr = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-          rs[e & 3] = __fadd2_rn(rs[e & 3], pr);
-          const __nv_bfloat162 two = __float22bfloat162_rn(pr);
-          pk[hh][e] = *reinterpret_cast<const uint32_t*>(&two);
-        }
-      const float2 r01 = __fadd2_rn(__fadd2_rn(rs[0], rs[1]), __fadd2_rn(rs[2], rs[3]));
-      l_sum += r01.x + r01.y;
-      // P and O are free once PV(i-1) has completed
-      if (i >= 1) {
-        ok = (warp_wait(smem_u32(pv_done), (i - 1) & 1, &abort_s));
+      for (int h = 0; h < 2; ++h) {               // 32 keys at a time
+        // (the partner has read this half of the tile before)
+        if (ok && i >= 1) ok = warp_wait<true>(smem_u32(&x_free[h]), (i - 1) & 1);
         if (!ok) break;
-        tc_fence_after();
-        if (__any_sync(0xffffffffu, need)) {       // O to the new reference
-          for (int c0 = 0; c0 < C::V_HALF; c0 += 32) {
-            uint32_t u[32];
-            tmem_ld32(lane_addr + c0, u);
-            tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * alpha);
-            tmem_st32(lane_addr + c0, u);
-          }
-        }
+        for (int g = 0; g < 8; ++g)
+          st_async_v4(dst + (h * 8 + g) * (64 * 16), su[h][4 * g], su[h][4 * g + 1],
+                      su[h][4 * g + 2], su[h][4 * g + 3], bar + (2 * (i & 1) + h) * 8);
       }
-      tmem_st16(lane_addr + C::P_COL, pk[0]);
-      tmem_st16(lane_addr + C::P_COL + 16, pk[1]);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(p_full));
     }
+    // (every arrival that the partner owes has landed before the CTA can leave)
+    for (int h = 0; h < 2 && ok && n > 0; ++h)
+      ok = warp_wait<true>(smem_u32(&x_free[h]), (n - 1) & 1);
     if (!ok) {
       abort_s = 1;
-      if (p.status) atomicOr(p.status, kStatusTimeout);
+      if (lane == 0 && p.status) atomicOr(p.status, kStatusTimeout);
     }
-    // ---- epilogue
-    const bool write = hrow < p.h;
+  } else {
+    // ------------------------------------------------------------ softmax of the CTA's heads
+    // Two warps a quarter take turns tile by tile; each hands the other the heads' references.
+    const int t = warp >> 2;
+    const int hrow = q * 32 + lane;             // head = TMEM lane
+    const int hloc = hrow & 63;
+    const bool head = hrow < p.h;               // (small shapes: MMA rows past the heads)
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const float4* xin = reinterpret_cast<const float4*>(sX) + hloc;
+    const uint32_t x_free_peer = map_to_rank(smem_u32(x_free), peer);
+    const uint32_t p_peer = map_to_rank(smem_u32(sP), peer) + t * C::P_BYTES + q * 32 * 128;
+    const uint32_t alpha_peer = map_to_rank(smem_u32(sAlpha + t * 64 + hloc), peer);
+    const uint32_t p_full_peer = map_to_rank(smem_u32(&p_full[t]), peer);
+    // (16-byte chunk g of the head's row lies at XOR 16 g)
+    const uint32_t p_own = smem_u32(sP) + t * C::P_BYTES + sw128_offset(hrow, 0);
+    const uint32_t p_rows = smem_u32(sP) + t * C::P_BYTES + q * 32 * 128;
+    const uint32_t xb = smem_u32(&x_full[2 * t]);
+    const bool counts = (q & 1) == 0;           // one of the tile's two warps expects the bytes
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+    float m_mine = -INFINITY, l_sum = 0.f;      // l_sum: this warp's tiles, to reference m_mine
+    bool ok = !abort_s;
+#pragma unroll 1
+    for (int i = t; i < n && ok; i += 2) {
+      const uint32_t ph = (i >> 1) & 1;
+      if (counts && lane == 0) {
+        mbar_arrive_expect_tx(xb, C::X_BYTES / 2);
+        mbar_arrive_expect_tx(xb + 8, C::X_BYTES / 2);
+      }
+      ok = warp_wait(smem_u32(&s_full[t]), ph);
+      if (!ok) break;
+      tc_fence_after();
+      float2 s[32];                               // the logits of 64 keys, two to a register pair
+      {
+        uint32_t su[2][32];
+        tmem_ld32(lane_addr + C::S_COL, su[0]);
+        tmem_ld32(lane_addr + C::S_COL + 32, su[1]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          s[e] = make_float2(__uint_as_float(su[e / 16][2 * (e % 16)]),
+                             __uint_as_float(su[e / 16][2 * (e % 16) + 1]));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(s_empty));
+      // ---- plus the partner's half of these logits, 32 keys at a time
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (ok) ok = warp_wait<true>(xb + h * 8, ph);
+        if (!ok) break;
+#pragma unroll
+        for (int g = 8 * h; g < 8 * h + 8; ++g) {
+          const float4 x = xin[g * 64];
+          s[2 * g] = __fadd2_rn(s[2 * g], make_float2(x.x, x.y));
+          s[2 * g + 1] = __fadd2_rn(s[2 * g + 1], make_float2(x.z, x.w));
+        }
+        // (the sums pin the loads before the arrival)
+#pragma unroll
+        for (int e = 16 * h; e < 16 * h + 16; ++e) asm volatile("" : "+f"(s[e].x), "+f"(s[e].y));
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(x_free_peer + h * 8);
+      }
+      if (!ok) break;
+      if (mask_of(i) != ~0ull) {                  // invalid keys: -inf, so p = 0
+        const uint64_t vmask = mask_of(i);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          if (!((vmask >> (2 * e)) & 1u)) s[e].x = -INFINITY;
+          if (!((vmask >> (2 * e + 1)) & 1u)) s[e].y = -INFINITY;
+        }
+      }
+      // ---- the heads' references: moved only when a tile beats them by 2^8 (p and the sums stay far
+      // inside fp32 and bf16 either way), handed on to the other warp before the exponentials
+      float mm[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mm[e] = fmaxf(s[e].x, s[e].y);
+#pragma unroll
+      for (int e = 4; e < 32; ++e) mm[e & 3] = fmaxf(fmaxf(mm[e & 3], s[e].x), s[e].y);
+      const float m_tile = fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * p.scale_log2;
+      float m_old = -INFINITY;
+      if (i >= 1) {
+        ok = warp_wait(smem_u32(&m_full[(q & 1) * 2 + (t ^ 1)]), ((i - 1) >> 1) & 1);
+        if (!ok) break;
+        m_old = sRef[(t ^ 1) * 64 + hloc];
+      }
+      const float m_ref = head && m_tile > m_old + 8.0f ? m_tile : m_old;
+      sRef[t * 64 + hloc] = m_ref;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&m_full[(q & 1) * 2 + t]));
+      if (i >= 2) ok = warp_wait<true>(smem_u32(&p_empty[t]), ph ^ 1u);   // both PV(i - 2)
+      if (!ok) break;
+      // ---- p = 2^(sigma log2e s - reference) into shared memory, two keys to an instruction.  The
+      // denominator sums the fp32 probabilities, only the PV operand is rounded (bf16: the MMA's
+      // operand type).
+      float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      const float nm = m_ref != -INFINITY ? -m_ref : 0.f;   // (-inf logits only: p = 0, not NaN)
+      const float2 nm2 = make_float2(nm, nm);
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {               // 8 keys: a 16-byte chunk of P
+        uint32_t pk[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 x = __ffma2_rn(s[4 * g + e], sc2, nm2);
+          const float2 pr = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+          rs[e & 1] = __fadd2_rn(rs[e & 1], pr);
+          const __nv_bfloat162 two = __float22bfloat162_rn(pr);
+          pk[e] = *reinterpret_cast<const uint32_t*>(&two);
+        }
+        st_shared_v4(p_own ^ (g * 16), pk[0], pk[1], pk[2], pk[3]);
+      }
+      const float2 sum = __fadd2_rn(rs[0], rs[1]);
+      fence_proxy_async_smem();                  // P, before MMAs and the copy read it
+      __syncwarp();
+      // the quarter's 32 rows of P (4 KB) to the partner
+      if (lane == 0)
+        bulk_copy_cluster(p_peer, p_rows, 32 * 128, p_full_peer);
+      const float alpha = m_ref != m_old ? exp2_approx(m_old - m_ref) : 1.f;
+      st_async(alpha_peer, __float_as_uint(alpha), p_full_peer);
+      if (m_ref != m_mine) l_sum *= exp2_approx(m_mine - m_ref);
+      m_mine = m_ref;
+      l_sum += sum.x + sum.y;
+      if (i >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {   // O to the new reference
+        ok = warp_wait(smem_u32(&pv_done[t ^ 1]), ((i - 1) >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        rescale_o<C::V_HALF>(lane_addr, alpha);
+        tc_fence_before();
+        __syncwarp();
+      }
+      if (lane == 0) {
+        if (counts) mbar_arrive_expect_tx(smem_u32(&p_full[t]), C::P_TX);
+        else mbar_arrive(smem_u32(&p_full[t]));
+      }
+    }
+    // (every arrival that the partner owes has landed before the CTA can leave)
+    const int uses = (n - t + 1) / 2;            // tiles of this warp
+    if (ok && uses > 0) ok = warp_wait<true>(smem_u32(&p_empty[t]), (uses - 1) & 1);
+    if (!ok) {
+      abort_s = 1;
+      if (lane == 0 && p.status) atomicOr(p.status, kStatusTimeout);
+    }
+    sSum[t * 128 + hloc] = l_sum;
+    sSum[t * 128 + 64 + hloc] = m_mine;
+  }
+  if (threadIdx.x == 0) mbar_wait(smem_u32(q_bar), 0, nullptr);   // Q has landed
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp < 4 && own) {
+    // ---- the heads' sums over both warps' tiles: 1 / sum for both CTAs, LSE
+    const int hrow = q * 32 + lane, hloc = hrow & 63;
+    const float m0 = sSum[64 + hloc], m1 = sSum[128 + 64 + hloc];
+    const float m = fmaxf(m0, m1);
+    const float l = (m0 == m ? sSum[hloc] : sSum[hloc] * exp2_approx(m0 - m)) +
+                    (m1 == m ? sSum[128 + hloc] : sSum[128 + hloc] * exp2_approx(m1 - m));
+    const bool any = n > 0 && !abort_s && !(l <= 0.f);      // (a NaN sum stays visible)
+    const float inv = any ? 1.f / l : 0.f;
+    const float lse = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    sInv[hrow] = inv;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_rank(smem_u32(sInv + hrow), peer)),
+                 "f"(inv)
+                 : "memory");
+    if (hrow < p.h) {
+      const int64_t prow = (static_cast<int64_t>(split) * p.row_count + r) * p.h + hrow;
+      if (p.part_lse != nullptr) p.part_lse[prow] = lse;
+      else p.lse[static_cast<int64_t>(row) * p.h + hrow] = lse;
+    }
+  }
+  __syncwarp();
+  cluster_sync();      // both CTAs are done; nothing remote is touched after this
+  {
+    // ------------------------------------------------------------ epilogue: O / sum
+    const int hrow = q * 32 + lane;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int64_t orow = static_cast<int64_t>(row) * p.h + hrow;
-    if (ok && n > 0)
-      ok = (warp_wait(smem_u32(pv_done), (n - 1) & 1, &abort_s));
-    tc_fence_after();
-    const bool any = ok && n > 0 && !(l_sum <= 0.f);   // (a NaN sum stays visible)
-    const float inv_l = any ? 1.f / l_sum : 0.f;
-    const float lse_v = any ? (m_ref + log2f(l_sum)) * 0.69314718055994531f : -INFINITY;
     const int64_t prow = (static_cast<int64_t>(split) * p.row_count + r) * p.h + hrow;
-    float* po = p.part_o != nullptr ? p.part_o + prow * D_V + vh * C::V_HALF : nullptr;
-    for (int c0 = 0; c0 < C::V_HALF; c0 += 32) {
+    float* po = p.part_o != nullptr ? p.part_o + prow * D_V + c * C::V_HALF : nullptr;
+    const float inv = sInv[hrow];
+    for (int c0 = (warp >> 2) * 32; c0 < C::V_HALF; c0 += 128) {
       float o[32];
-      if (ok && n > 0) {                          // (warp-uniform: the TMEM load is collective)
+      if (n > 0) {                                // (uniform: the TMEM load is collective)
         uint32_t u[32];
         tmem_ld32(lane_addr + c0, u);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = any ? __uint_as_float(u[j]) * inv_l : 0.f;
+        for (int j = 0; j < 32; ++j) o[j] = inv != 0.f ? __uint_as_float(u[j]) * inv : 0.f;
       } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = 0.f;
       }
-      if (!write) continue;
+      if (hrow >= p.h) continue;
       if (po != nullptr) {
 #pragma unroll
         for (int j = 0; j < 32; j += 4)
           *reinterpret_cast<float4*>(po + c0 + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
       } else {
-        __nv_bfloat16* dst = p.out + orow * D_V + vh * C::V_HALF + c0;
+        __nv_bfloat16* dst = p.out + orow * D_V + c * C::V_HALF + c0;
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
           uint32_t pk[4];
@@ -688,12 +908,7 @@ __global__ void __launch_bounds__(512, 1)
         }
       }
     }
-    if (write && vh == 0) {
-      if (p.part_lse != nullptr) p.part_lse[prow] = lse_v;
-      else p.lse[orow] = lse_v;
-    }
   }
-  if (threadIdx.x == 0) mbar_wait(smem_u32(q_bar), 0, nullptr);   // Q has landed
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
