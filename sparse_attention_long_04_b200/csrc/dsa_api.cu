@@ -1508,7 +1508,7 @@ dsa_status_t dsa_cache_read_q8(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
   prm.total_keys = total_keys;
   prm.status = dev_status;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(ceil_div(total_keys, 8));
+  const unsigned grid = static_cast<unsigned>(ceil_div(total_keys, 8 * kReadKeys));
   if (dims->d_qk == 576)
     dsa_cache_read_kernel<576, 512><<<grid, 256, 0, st>>>(prm);
   else

@@ -606,10 +606,10 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
       for (int ks = 0; ks < C::VKB; ++ks) {
         uint8_t* at = dst + ks * C::KB_BYTES;
-        uint4 lo, hi;
-        q8_expand16(x.code[ks], x.scale[ks / 2], lo, hi);
-        *reinterpret_cast<uint4*>(at + sw128_offset(rl, 2 * cl)) = lo;
-        *reinterpret_cast<uint4*>(at + sw128_offset(rl, 2 * cl + 1)) = hi;
+        *reinterpret_cast<uint4*>(at + sw128_offset(rl, 2 * cl)) =
+            q8_expand8(make_uint2(x.code[ks].x, x.code[ks].y), x.scale[ks / 2]);
+        *reinterpret_cast<uint4*>(at + sw128_offset(rl, 2 * cl + 1)) =
+            q8_expand8(make_uint2(x.code[ks].z, x.code[ks].w), x.scale[ks / 2]);
       }
     };
     bool ok = true;

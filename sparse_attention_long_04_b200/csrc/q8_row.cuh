@@ -72,27 +72,25 @@ __device__ __forceinline__ uint2 q8_expand4(uint32_t w, __nv_bfloat162 mul) {
                     q8_expand2(__byte_perm(w, 0, 0x4342), mul));
 }
 
-// Sixteen codes (one 16-byte chunk of a group with scale s) as sixteen bf16.  2^120 s is a bf16
-// up to s = 2^7; larger scales (and the NaN scale) multiply in two steps.
-__device__ __forceinline__ void q8_expand16(const uint4& c, float s, uint4& lo, uint4& hi) {
+// Eight codes of a group with scale s as eight bf16.  2^120 s is a bf16 up to s = 2^7; larger
+// scales (and the NaN scale) multiply in two steps.
+__device__ __forceinline__ uint4 q8_expand8(uint2 c, float s) {
   const uint32_t sb = __float_as_uint(s);
   const bool big = sb > 0x43000000u;              // s > 2^7, or the NaN scale
   // the upper half of an fp32 power of two is its bf16
   const uint32_t mb = __byte_perm((big ? 0x43000000u : sb) + (120u << 23), 0, 0x3232);
   const __nv_bfloat162 mul = *reinterpret_cast<const __nv_bfloat162*>(&mb);
-  uint2 e[4] = {q8_expand4(c.x, mul), q8_expand4(c.y, mul), q8_expand4(c.z, mul),
-                q8_expand4(c.w, mul)};
+  uint2 e[2] = {q8_expand4(c.x, mul), q8_expand4(c.y, mul)};
   if (big) {
     const __nv_bfloat162 m2 = __float2bfloat162_rn(s * 0x1p-7f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&e[i].x), m2);
       const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&e[i].y), m2);
       e[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
     }
   }
-  lo = make_uint4(e[0].x, e[0].y, e[1].x, e[1].y);
-  hi = make_uint4(e[2].x, e[2].y, e[3].x, e[3].y);
+  return make_uint4(e[0].x, e[0].y, e[1].x, e[1].y);
 }
 
 }  // namespace dsa
