@@ -21,7 +21,10 @@
 // epilogue.  Key stages are a ring of STAGES buffers; the
 // accumulators are a ring of ACC buffers in TMEM so the epilogue of tile i overlaps the MMA of
 // later tiles.  Decode (one query row, N = 64) runs two epilogue warpgroups on alternate tiles;
-// prefill (N = 256) splits each tile's columns over four warpgroups, one query row each.
+// prefill and chunks (N = 256) split each tile's columns over four warpgroups, one query row each:
+// 512 rows x 65536 keys in 412 us, 1650 cycles a tile, of which the MMAs take 512.  The epilogue
+// bounds it: 64 maxima and 32 packed FMAs a thread and tile are 740 cycles of a scheduler's time
+// over its four warps (maxima 2 cycles, packed FMAs 3), the waits and loads around them the rest.
 //
 // Fused first digit of the top-k (when `hist` is given): as it writes a score, each epilogue
 // thread also counts it in its query row's histogram of the top 11 bits of the order-preserving
@@ -79,9 +82,15 @@ struct IndexerCfg {
   // more page copies moving than one issuing thread does
   static constexpr int PRODUCERS = QPG == 1 || kChunk ? 2 : 1;
   static constexpr int ACC = QPG == 1 ? 4 : 2;        // TMEM accumulator ring
-  static constexpr int EPI_WARPS = QPG == 1 ? 8 : 16;    // prefill: one query row per warpgroup
-  static constexpr bool TILE_SPLIT = QPG == 1;        // warpgroups take alternate tiles
+  static constexpr int EPI_WARPS = QPG == 1 ? 8 : 16;
+  static constexpr bool TILE_SPLIT = QPG == 1;        // a warp's scores one tile at a time
   static constexpr int EPI_PER_TILE = TILE_SPLIT ? 4 : EPI_WARPS;   // warps reading one tile
+  // One query row per warpgroup: its factors c[t,j] stay in registers, and every thread loads its
+  // key's scale from the cache itself, a tile ahead.  With both in shared memory (16 broadcast
+  // loads of 16 bytes a lane and tile, 4 cycles of the SM's load path each; the scale behind the
+  // tile's barrier) 512 rows x 65536 keys take 435 us, with c alone in registers 458, so 412.
+  static constexpr bool REG_C = !TILE_SPLIT && H_I == 64;
+  static_assert(!REG_C || QPG * 4 == EPI_WARPS, "a query row per warpgroup");
   static constexpr int THREADS = (4 + EPI_WARPS) * 32;
   static constexpr int TILE_BYTES = 128 * D_I;        // 128 keys
   static constexpr int Q_BYTES = N * D_I;
@@ -220,11 +229,11 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
-      mbar_init(smem_u32(&empty[i]), 1 + C::EPI_PER_TILE);
+      mbar_init(smem_u32(&empty[i]), C::REG_C ? 1 : 1 + C::EPI_PER_TILE);
     }
     for (int i = 0; i < C::ACC; ++i) {
       mbar_init(smem_u32(&tfull[i]), 1);
-      mbar_init(smem_u32(&tempty[i]), C::TILE_SPLIT ? 4 : C::EPI_WARPS);
+      mbar_init(smem_u32(&tempty[i]), C::EPI_PER_TILE);
     }
     mbar_init(smem_u32(qbar), 1);
     mbar_init(smem_u32(done), 1);
@@ -269,7 +278,7 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
       for (int it = pr; it < n_tiles; it += C::PRODUCERS) {
         const int s = it % C::STAGES;
         if (it >= C::STAGES &&
-            !mbar_wait(smem_u32(&empty[s]), ((it / C::STAGES) - 1) & 1, &abort_s)) {
+            !thread_wait(smem_u32(&empty[s]), ((it / C::STAGES) - 1) & 1)) {
           abort_s = 1;
           if (p.status) atomicOr(p.status, kStatusTimeout);
           break;
@@ -282,7 +291,9 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
           const int64_t y = static_cast<int64_t>(p.key0) + tile * 128;
           const int64_t a0 = y & ~int64_t(3);
           const int64_t avail = p.num_kv_rows - a0;
-          const uint32_t sb = static_cast<uint32_t>((avail < 132 ? avail : int64_t(132)) / 4 * 16);
+          const uint32_t sb =
+              C::REG_C ? 0u
+                       : static_cast<uint32_t>((avail < 132 ? avail : int64_t(132)) / 4 * 16);
           const int lead = static_cast<int>(y - a0);
           for (int hlf = 0; hlf < 2; ++hlf) {
             sRow0[s * 2 + hlf] = y + hlf * 64;
@@ -319,7 +330,7 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
               sRow0[s * 2 + hlf] = y[hlf];
               sFirst[s * 2 + hlf] = hlf * 80;
               sValid[s * 2 + hlf] = ok[hlf] ? 64 : 0;
-              bytes += ok[hlf] ? 64 * D_I + 256 : 0;
+              bytes += ok[hlf] ? 64 * D_I + (C::REG_C ? 0 : 256) : 0;
             }
             mbar_arrive_expect_tx(smem_u32(&full[s]), bytes);
             for (int hlf = 0; hlf < 2; ++hlf) {
@@ -329,7 +340,8 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
               const uint8_t* scales = p.k_blocks + blk * kBlockBytes + 64 * D_I;
               if constexpr (kChunk) {              // other groups read the same pages: keep them
                 tma_load_3d(kdst, &kmap, smem_u32(&full[s]), 0, 0, static_cast<int32_t>(blk));
-                bulk_load_g2s(smem_u32(sbuf + hlf * 80), scales, 256, smem_u32(&full[s]));
+                if constexpr (!C::REG_C)
+                  bulk_load_g2s(smem_u32(sbuf + hlf * 80), scales, 256, smem_u32(&full[s]));
               } else {
                 tma_load_3d_hint(kdst, &kmap, smem_u32(&full[s]), 0, 0, static_cast<int32_t>(blk),
                                  pol);
@@ -344,7 +356,9 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
           for (int hlf = 0; hlf < 2; ++hlf) {
             a0[hlf] = y[hlf] & ~int64_t(3);
             const int64_t avail = p.num_kv_rows - a0[hlf];
-            sb[hlf] = ok[hlf] ? static_cast<uint32_t>((avail < 68 ? avail : int64_t(68)) / 4 * 16) : 0u;
+            sb[hlf] = ok[hlf] && !C::REG_C
+                          ? static_cast<uint32_t>((avail < 68 ? avail : int64_t(68)) / 4 * 16)
+                          : 0u;
             const int lead = static_cast<int>(y[hlf] - a0[hlf]);
             sRow0[s * 2 + hlf] = y[hlf];
             sFirst[s * 2 + hlf] = hlf * 80 + lead;
@@ -402,64 +416,52 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
     if (pr == 0 && lane == 0) mbar_wait(smem_u32(qbar), 0, nullptr);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_f32acc(0 /* e4m3 */, 128, N, 0, 0);
-      bool ok = mbar_wait(smem_u32(qbar), 0, &abort_s);
-      for (int it = 0; ok && it < n_tiles; ++it) {
-        const int s = it % C::STAGES;
-        const int a = it % C::ACC;
-        ok = mbar_wait(smem_u32(&full[s]), (it / C::STAGES) & 1, &abort_s);
-        if (ok && it >= C::ACC)
-          ok = mbar_wait(smem_u32(&tempty[a]), ((it / C::ACC) - 1) & 1, &abort_s);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t kaddr = smem_u32(sK + s * C::TILE_BYTES);
-        const uint32_t qaddr = smem_u32(sQ);
+    constexpr uint32_t idesc = idesc_f32acc(0 /* e4m3 */, 128, N, 0, 0);
+    const uint64_t kd = sdesc(smem_u32(sK), 16, C::SBO, C::LAYOUT);
+    const uint64_t qd = sdesc(smem_u32(sQ), 16, C::SBO, C::LAYOUT);
+    bool ok = warp_wait(smem_u32(qbar), 0);
+    for (int it = 0; ok && it < n_tiles; ++it) {
+      const int s = it % C::STAGES;
+      const int a = it % C::ACC;
+      ok = warp_wait(smem_u32(&full[s]), (it / C::STAGES) & 1) &&
+           (it < C::ACC || warp_wait(smem_u32(&tempty[a]), ((it / C::ACC) - 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {                       // (32 bytes of each row a step)
 #pragma unroll
         for (int k = 0; k < C::KSTEPS; ++k)
-          umma_e4m3(tmem + a * N, sdesc(kaddr + k * 32, 16, C::SBO, C::LAYOUT),
-                    sdesc(qaddr + k * 32, 16, C::SBO, C::LAYOUT), idesc, k > 0);
+          umma_e4m3(tmem + a * N, kd + s * (C::TILE_BYTES / 16) + k * 2, qd + k * 2, idesc, k > 0);
         umma_commit(smem_u32(&empty[s]));
         umma_commit(smem_u32(&tfull[a]));
       }
-      if (!ok) {
-        abort_s = 1;
-        if (p.status) atomicOr(p.status, kStatusTimeout);
-      }
-      umma_commit(smem_u32(done));
-      mbar_wait(smem_u32(done), 0, nullptr);
+      __syncwarp();
     }
+    if (!ok) {
+      abort_s = 1;
+      if (lane == 0 && p.status) atomicOr(p.status, kStatusTimeout);
+    }
+    __syncwarp();
+    if (elect_one()) umma_commit(smem_u32(done));
+    __syncwarp();
+    warp_wait(smem_u32(done), 0);
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ epilogue
-    constexpr int PARTS = C::TILE_SPLIT ? 1 : C::EPI_WARPS / 4;
+    constexpr int PARTS = C::EPI_PER_TILE / 4;
     constexpr int COLS = N / PARTS;          // columns this warp reduces
     const int quad = warp & 3;               // TMEM lanes 32*quad .. 32*quad+31
     const int grp = (warp - 4) / 4;          // warpgroup
     const int part = C::TILE_SPLIT ? 0 : grp;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint64_t slab_pol = l2_evict_last();   // the decode slab stays in L2 for the top-k
-    for (int it = C::TILE_SPLIT ? grp : 0; it < n_tiles; it += C::TILE_SPLIT ? 2 : 1) {
-      const int a = it % C::ACC;
+    // the scale of this thread's key of tile `it`, which comes with the tile's keys
+    auto key_scale = [&](int it, float& ks) -> bool {
       const int s = it % C::STAGES;
-      if (!mbar_wait(smem_u32(&tfull[a]), (it / C::ACC) & 1, &abort_s)) {
-        abort_s = 1;
-        if (p.status) atomicOr(p.status, kStatusTimeout);
-        break;
-      }
-      tc_fence_after();
-      // the tile's scales came with its keys: observe that phase of full[s] (the stage is not
-      // refilled before this warp releases it below)
-      if (!mbar_wait(smem_u32(&full[s]), (it / C::STAGES) & 1, &abort_s)) {
-        abort_s = 1;
-        if (p.status) atomicOr(p.status, kStatusTimeout);
-        break;
-      }
+      if (!warp_wait(smem_u32(&full[s]), (it / C::STAGES) & 1)) return false;
       const int kin = quad * 32 + lane;        // key within the tile
-      const int key = (t_begin + it) * 128 + kin;
       const int hb = kin >> 6;
       const int j = kin & 63;
-      float ks = 0.f;
-      if (key < n_keys) {
+      ks = 0.f;
+      if ((t_begin + it) * 128 + kin < n_keys) {
         if (j < sValid[s * 2 + hb]) {
           ks = sScale[s * C::SCALE_FLOATS + sFirst[s * 2 + hb] + j];
         } else {                               // the last rows of the cache: not bulk-copied
@@ -468,100 +470,160 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
                                                                           : 0.f;
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&empty[s]));
-      if constexpr (!C::TILE_SPLIT && H_I >= 32 && H_I % 32 == 0) {
-        // all of this warp's columns in one TMEM round trip; the accumulator is free again
-        // before the arithmetic starts
-        constexpr int NCH = COLS / 32;
-        uint32_t r[NCH][32];
+      return true;
+    };
+    auto give_up = [&] {
+      abort_s = 1;
+      if (p.status) atomicOr(p.status, kStatusTimeout);
+    };
+    if constexpr (C::REG_C) {
+      float2 c_row[H_I / 2];
 #pragma unroll
-        for (int c = 0; c < NCH; ++c) tmem_ld32(lane_addr + a * N + part * COLS + c * 32, r[c]);
-        tmem_wait_ld();
-        tc_fence_before();
+      for (int j = 0; j < H_I / 2; ++j) c_row[j] = reinterpret_cast<const float2*>(sC + part * H_I)[j];
+      const bool row_in = part < rows_in_group;
+      float* out = p.scores + static_cast<int64_t>(p.out_row0 + (grow0 - p.row0) + part) * p.ld;
+      // The key scales come straight from the cache, two steps ahead of their use: the cache row of
+      // the warp's 64-key half of tile it + 2 and the scale of this thread's key of tile it + 1 are
+      // loaded under tile it.
+      const int half = quad >> 1;
+      const int n_halves = (n_keys + 63) / 64;
+      const int32_t* table =
+          kChunk && p.block_table != nullptr
+              ? p.block_table + static_cast<int64_t>(b) * p.max_blocks : nullptr;
+      const int64_t first = kChunk ? seq_base : p.key0;   // without a table: the sequence's first row
+      auto block_of = [&](int it) -> int32_t {       // -1: none
+        const int blk = (t_begin + it) * 2 + half;
+        if (it >= n_tiles || blk >= n_halves) return -1;
+        return table != nullptr ? __ldg(table + blk) : blk;
+      };
+      auto scale_of = [&](int32_t blk) -> float {
+        const int j = (quad & 1) * 32 + lane;
+        const int64_t row = (table != nullptr ? 0 : first) + static_cast<int64_t>(blk) * 64 + j;
+        if (blk < 0 || row >= p.num_kv_rows) return 0.f;
+        return p.k_scale != nullptr
+                   ? __ldg(p.k_scale + row)
+                   : __ldg(reinterpret_cast<const float*>(
+                               p.k_blocks + static_cast<int64_t>(blk) * (64 * (D_I + 4)) + 64 * D_I) + j);
+      };
+      float ks = scale_of(block_of(0));
+      int32_t blk_next = block_of(1);
+      bool ok = true;
+      for (int it = 0; ok && it < n_tiles; ++it) {
+        const int a = it % C::ACC;
+        const float ks_now = ks;
+        ok = warp_wait(smem_u32(&tfull[a]), (it / C::ACC) & 1);
+        if (!ok) {
+          give_up();
+          break;
+        }
+        tc_fence_after();
+        const uint32_t acc = lane_addr + a * N + part * H_I;
+        // heads in pairs: one packed fp32x2 FMA per two heads (the ReLU stays scalar), eight
+        // heads loaded while eight are added
+        float2 a01 = make_float2(0.f, 0.f), a23 = make_float2(0.f, 0.f);
+        uint32_t r[2][8];
+        tmem_ld8(acc, r[0]);
+        ks = scale_of(blk_next);
+        blk_next = block_of(it + 2);
+#pragma unroll
+        for (int c = 0; c < H_I / 8; ++c) {
+          tmem_wait_ld();
+          if (c + 1 < H_I / 8) {
+            tmem_ld8(acc + (c + 1) * 8, r[(c + 1) & 1]);
+          } else {                             // the accumulator is free again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
+          }
+          const uint32_t(&x)[8] = r[c & 1];
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
+            a01 = __ffma2_rn(c_row[(c * 8 + j) / 2],
+                             make_float2(fmaxf(__uint_as_float(x[j + 0]), 0.f),
+                                         fmaxf(__uint_as_float(x[j + 1]), 0.f)),
+                             a01);
+            a23 = __ffma2_rn(c_row[(c * 8 + j) / 2 + 1],
+                             make_float2(fmaxf(__uint_as_float(x[j + 2]), 0.f),
+                                         fmaxf(__uint_as_float(x[j + 3]), 0.f)),
+                             a23);
+          }
+        }
+        const int key = (t_begin + it) * 128 + quad * 32 + lane;
+        if (row_in && key <= pos_first + part) {
+          const float sc = ks_now * ((a01.x + a01.y) + (a23.x + a23.y));
+          out[key] = sc;
+          if (hist_on) atomicAdd(&sHist[part * kIdxHistBins + (order_key(sc) >> 21)], 1u);
+        }
+      }
+    } else {
+      for (int it = C::TILE_SPLIT ? grp : 0; it < n_tiles; it += C::TILE_SPLIT ? 2 : 1) {
+        const int a = it % C::ACC;
+        const int s = it % C::STAGES;
+        float ks;
+        if (!key_scale(it, ks)) {
+          give_up();
+          break;
+        }
+        const int key = (t_begin + it) * 128 + quad * 32 + lane;
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
-        constexpr int CPR = H_I / 32;          // chunks per query row
-#pragma unroll
-        for (int q = 0; q < NCH / CPR; ++q) {
-          // heads in pairs: one packed fp32x2 FMA per two heads (ReLU stays scalar)
-          float2 a01 = make_float2(0.f, 0.f), a23 = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int c = q * CPR; c < (q + 1) * CPR; ++c) {
-            const float4* cc = reinterpret_cast<const float4*>(sC + part * COLS + c * 32);
+        if (lane == 0) mbar_arrive(smem_u32(&empty[s]));
+        if (!warp_wait(smem_u32(&tfull[a]), (it / C::ACC) & 1)) {
+          give_up();
+          break;
+        }
+        tc_fence_after();
+        float2 a01 = make_float2(0.f, 0.f), a23 = make_float2(0.f, 0.f);   // heads in pairs
+#pragma unroll 1
+        for (int c0 = 0; c0 < COLS; c0 += 32) {
+          const int col = part * COLS + c0;
+          uint32_t r[32];
+          tmem_ld32(lane_addr + a * N + col, r);
+          tmem_wait_ld();
+          const float4* cc = reinterpret_cast<const float4*>(sC + col);
+          if constexpr (H_I >= 32) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
               const float4 c4 = cc[j / 4];
               a01 = __ffma2_rn(make_float2(c4.x, c4.y),
-                               make_float2(fmaxf(__uint_as_float(r[c][j + 0]), 0.f),
-                                           fmaxf(__uint_as_float(r[c][j + 1]), 0.f)),
+                               make_float2(fmaxf(__uint_as_float(r[j + 0]), 0.f),
+                                           fmaxf(__uint_as_float(r[j + 1]), 0.f)),
                                a01);
               a23 = __ffma2_rn(make_float2(c4.z, c4.w),
-                               make_float2(fmaxf(__uint_as_float(r[c][j + 2]), 0.f),
-                                           fmaxf(__uint_as_float(r[c][j + 3]), 0.f)),
+                               make_float2(fmaxf(__uint_as_float(r[j + 2]), 0.f),
+                                           fmaxf(__uint_as_float(r[j + 3]), 0.f)),
                                a23);
             }
-          }
-          const int rr = (part * COLS) / H_I + q;
-          if (rr < rows_in_group && key <= pos_first + rr) {
-            const float sc = ks * ((a01.x + a01.y) + (a23.x + a23.y));
-            p.scores[static_cast<int64_t>(p.out_row0 + (grow0 - p.row0) + rr) * p.ld + key] = sc;
-            if (hist_on) atomicAdd(&sHist[rr * kIdxHistBins + (order_key(sc) >> 21)], 1u);
-          }
-        }
-        continue;
-      }
-      float2 a01 = make_float2(0.f, 0.f), a23 = make_float2(0.f, 0.f);   // heads in pairs
-#pragma unroll 1
-      for (int c0 = 0; c0 < COLS; c0 += 32) {
-        const int col = part * COLS + c0;
-        uint32_t r[32];
-        tmem_ld32(lane_addr + a * N + col, r);
-        tmem_wait_ld();
-        const float4* cc = reinterpret_cast<const float4*>(sC + col);
-        if constexpr (H_I >= 32) {
+            if ((col + 32) % H_I == 0) {       // a query row's heads are complete
+              const int rr = col / H_I;
+              const float acc = (a01.x + a01.y) + (a23.x + a23.y);
+              a01 = make_float2(0.f, 0.f);
+              a23 = make_float2(0.f, 0.f);
+              if (rr < rows_in_group && key <= pos_first + rr) {
+                const float sc = ks * acc;
+                float* dst = p.scores + static_cast<int64_t>(p.out_row0 + (grow0 - p.row0) + rr) * p.ld + key;
+                if (C::TILE_SPLIT) st_global_hint(dst, sc, slab_pol);   // decode: read next
+                else *dst = sc;
+                if (hist_on) atomicAdd(&sHist[rr * kIdxHistBins + (order_key(sc) >> 21)], 1u);
+              }
+            }
+          } else {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 c4 = cc[j / 4];
-            a01 = __ffma2_rn(make_float2(c4.x, c4.y),
-                             make_float2(fmaxf(__uint_as_float(r[j + 0]), 0.f),
-                                         fmaxf(__uint_as_float(r[j + 1]), 0.f)),
-                             a01);
-            a23 = __ffma2_rn(make_float2(c4.z, c4.w),
-                             make_float2(fmaxf(__uint_as_float(r[j + 2]), 0.f),
-                                         fmaxf(__uint_as_float(r[j + 3]), 0.f)),
-                             a23);
-          }
-          if ((col + 32) % H_I == 0) {       // a query row's heads are complete
-            const int rr = col / H_I;
-            const float acc = (a01.x + a01.y) + (a23.x + a23.y);
-            a01 = make_float2(0.f, 0.f);
-            a23 = make_float2(0.f, 0.f);
-            if (rr < rows_in_group && key <= pos_first + rr) {
-              const float sc = ks * acc;
-              float* dst = p.scores + static_cast<int64_t>(p.out_row0 + (grow0 - p.row0) + rr) * p.ld + key;
-              if (C::TILE_SPLIT) st_global_hint(dst, sc, slab_pol);   // decode: read next
-              else *dst = sc;
-              if (hist_on) atomicAdd(&sHist[rr * kIdxHistBins + (order_key(sc) >> 21)], 1u);
+            for (int q = 0; q < 32 / H_I; ++q) {
+              float sacc = 0.f;
+#pragma unroll
+              for (int j = 0; j < H_I; ++j)
+                sacc = fmaf(sC[col + q * H_I + j], fmaxf(__uint_as_float(r[q * H_I + j]), 0.f), sacc);
+              const int rr = col / H_I + q;
+              if (rr < rows_in_group && key <= pos_first + rr)
+                p.scores[static_cast<int64_t>(p.out_row0 + (grow0 - p.row0) + rr) * p.ld + key] =
+                    ks * sacc;
             }
           }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 32 / H_I; ++q) {
-            float sacc = 0.f;
-#pragma unroll
-            for (int j = 0; j < H_I; ++j)
-              sacc = fmaf(sC[col + q * H_I + j], fmaxf(__uint_as_float(r[q * H_I + j]), 0.f), sacc);
-            const int rr = col / H_I + q;
-            if (rr < rows_in_group && key <= pos_first + rr)
-              p.scores[static_cast<int64_t>(p.out_row0 + (grow0 - p.row0) + rr) * p.ld + key] =
-                  ks * sacc;
-          }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
     }
   }
   tc_fence_before();

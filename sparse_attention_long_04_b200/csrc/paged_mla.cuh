@@ -62,71 +62,6 @@ struct PagedMlaParams {
 
 constexpr int kMaxDenseTiles = 2048;   // tiles of one split without idx
 
-// True in one lane of the (converged) warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
-constexpr uint32_t kPollNs = 1000, kPolls = 1u << 22;   // see warp_wait
-
-// One poll of `bar` by every lane; kHint: the lanes may sleep until the phase completes (or
-// kPollNs).  kCluster: acquires what the other CTA of the cluster wrote before it arrived.
-template <bool kCluster, bool kHint>
-__device__ __forceinline__ uint32_t poll_bar(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  if constexpr (kHint && kCluster)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(bar), "r"(parity), "r"(kPollNs) : "memory");
-  else if constexpr (kHint)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(bar), "r"(parity), "r"(kPollNs) : "memory");
-  else if constexpr (kCluster)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok;
-}
-
-// Whole-warp wait for phase `parity` of `bar`; all lanes return the same result, false when the
-// wait gave up.  The first poll has no suspend-time hint, which a completed phase answers in 14
-// cycles (46 with the hint, 195 for a poll by lane 0 and a shuffle); the polls after it sleep up
-// to kPollNs, so that waiting warps leave the pipes to the others, and are kPolls at most: at
-// least 40 ms of 20-cycle polls, at most some 4 s of full sleeps.  The limit is a count, not a
-// clock, to keep the many inlined copies short: the kernel's loops compete for the instruction
-// caches.
-template <bool kCluster = false>
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok = poll_bar<kCluster, false>(bar, parity);
-  if (!ok) {
-    uint32_t left = kPolls;
-#pragma unroll 1
-    do {
-      ok = poll_bar<kCluster, true>(bar, parity);
-    } while (!ok && --left != 0);
-  }
-  return __all_sync(0xffffffffu, ok) != 0;
-}
-
 // Asynchronous stores into a CTA of the cluster (addr and bar are shared::cluster addresses of
 // that CTA); the bytes are counted on its barrier when they have landed.
 __device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,

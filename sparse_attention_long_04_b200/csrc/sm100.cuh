@@ -114,6 +114,78 @@ __device__ __forceinline__ bool warp_mbar_wait(uint32_t bar, uint32_t parity,
   return ok != 0;
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+constexpr uint32_t kPollNs = 1000, kPolls = 1u << 22;   // see warp_wait
+
+// One poll of `bar` by every lane; kHint: the lanes may sleep until the phase completes (or
+// kPollNs).  kCluster: acquires what the other CTA of the cluster wrote before it arrived.
+template <bool kCluster, bool kHint>
+__device__ __forceinline__ uint32_t poll_bar(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (kHint && kCluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity), "r"(kPollNs) : "memory");
+  else if constexpr (kHint)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity), "r"(kPollNs) : "memory");
+  else if constexpr (kCluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok;
+}
+
+// Whole-warp wait for phase `parity` of `bar`; all lanes return the same result, false when the
+// wait gave up.  The first poll has no suspend-time hint, which a completed phase answers in 14
+// cycles (46 with the hint, 195 for a poll by lane 0 and a shuffle); the polls after it sleep up
+// to kPollNs, so that waiting warps leave the pipes to the others, and are kPolls at most: at
+// least 40 ms of 20-cycle polls, at most some 4 s of full sleeps.  The limit is a count, not a
+// clock, to keep the many inlined copies short: the kernel's loops compete for the instruction
+// caches.
+template <bool kCluster = false>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok = poll_bar<kCluster, false>(bar, parity);
+  if (!ok) {
+    uint32_t left = kPolls;
+#pragma unroll 1
+    do {
+      ok = poll_bar<kCluster, true>(bar, parity);
+    } while (!ok && --left != 0);
+  }
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// The same wait by one thread.
+__device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok = poll_bar<false, false>(bar, parity);
+  for (uint32_t left = kPolls; !ok && left != 0; --left) ok = poll_bar<false, true>(bar, parity);
+  return ok != 0;
+}
+
 // Barrier `id` (1..15; 0 is __syncthreads) over `count` threads (a multiple of 32): the warps
 // of a subset of the CTA, each arriving whole.
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t count) {
@@ -394,6 +466,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
         "=r"(r[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
       : "r"(taddr));
 }
 
