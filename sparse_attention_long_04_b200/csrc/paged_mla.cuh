@@ -148,7 +148,10 @@ struct PagedCfg {
   static_assert(V_HALF % 64 == 0 && V_HALF <= 256, "PV MMA N");
   static_assert(2 * VKB + 1 == KB_ALL, "value blocks and one rotary block");
   static_assert(TMEM_USED <= 512, "TMEM columns");
-  static_assert((VKB + 1) * Q_KB_BYTES <= V_SLOTS * V_SLOT_BYTES, "Q staging fits the ring");
+  static constexpr int Q_OFF = V_SLOTS * V_SLOT_BYTES - (VKB + 1) * Q_KB_BYTES;   // Q staging
+  static constexpr int PRE_TILES = Q_OFF / V_SLOT_BYTES;      // slots in front of it
+  static_assert(Q_OFF >= 0, "Q staging fits the ring");
+  static_assert(128 * (V_HALF * 4 + 16) <= V_SLOTS * V_SLOT_BYTES, "output staging fits the ring");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -176,7 +179,8 @@ __global__ void __launch_bounds__(512, 1)
   constexpr int ROW_BYTES = kQ8 ? R::BYTES : D_QK * 2;
   static_assert(R::ROPE <= 64 && D_V % 128 == 0, "rotary dims fill (part of) the last k-block");
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* sV = smem;                                           // [V_SLOTS] (Q staging first)
+  uint8_t* sV = smem;                                           // [V_SLOTS]
+  uint8_t* sQ = sV + C::Q_OFF;                                  // Q, before the ring needs it
   uint8_t* sR = sV + C::V_SLOTS * C::V_SLOT_BYTES;              // rotary block of a tile
   uint8_t* sP = sR + C::KB_BYTES;                               // [2] probabilities, all heads
   uint8_t* sX = sP + 2 * C::P_BYTES;   // [16 key quads][64 heads][4]: the partner's half logits
@@ -220,95 +224,70 @@ __global__ void __launch_bounds__(512, 1)
   const bool dense = p.idx == nullptr;
   const int n_tiles_all = p.topk / C::BN;
 
-  // ---- row geometry; the selected keys' indices (8 per thread of warps 8-15) are loaded first,
-  // so that their latency overlaps it and the set-up
-  constexpr int KPT = C::MAX_TILES * C::BN / 256;
-  int v[KPT];
+  // ---- the selected keys' indices, loaded first: warp 8 + pw resolves tiles pw, pw + 8, ...
+  constexpr int TPW = C::MAX_TILES / 8;
+  int v[2 * TPW];
   if (warp >= 8 && !dense) {
-    const int32_t* irow = p.idx + static_cast<int64_t>(r) * p.topk;
+    const int32_t* irow = p.idx + static_cast<int64_t>(r) * p.topk + lane;
 #pragma unroll
-    for (int j = 0; j < KPT; ++j) {
-      const int e = static_cast<int>(threadIdx.x) - 256 + 256 * j;
-      v[j] = e < p.topk ? irow[e] : -1;
+    for (int j = 0; j < TPW; ++j) {
+      const int tt = warp - 8 + 8 * j;
+      v[2 * j] = tt < n_tiles_all ? irow[tt * C::BN] : -1;
+      v[2 * j + 1] = tt < n_tiles_all ? irow[tt * C::BN + 32] : -1;
     }
+  }
+  // ---- set-up, under those loads
+  if (threadIdx.x == 0) {
+    // Q: the rotary block and the CTA's value blocks into the end of the (still idle) ring, h rows a
+    // block (lanes past h hold whatever was there and are never written out)
+    mbar_init(smem_u32(q_bar), 1);
+    fence_mbar_init();
+    const uint32_t kb_bytes = static_cast<uint32_t>(p.h) * 128u;
+    tma_prefetch_desc(&q_map);
+    mbar_arrive_expect_tx(smem_u32(q_bar), (C::VKB + 1) * kb_bytes);
+    for (int j = 0; j <= C::VKB; ++j)
+      tma_load_2d(smem_u32(sQ + j * C::Q_KB_BYTES), &q_map, smem_u32(q_bar),
+                  (j == 0 ? C::KB_ALL - 1 : c * C::VKB + j - 1) * 128, r * p.h);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(bars + 36), C::TMEM_COLS);
+  if (warp == 2) {
+    for (int i = lane; i < 35; i += 32) {
+      const uint64_t* bar = bars + i;
+      const bool gather = bar < v_empty || bar == r_full;
+      const bool pairs = bar >= x_free && bar < o_ok;       // x_free, p_full, p_empty
+      mbar_init(smem_u32(bar), gather ? C::GATHER : bar == s_empty ? 4 : pairs ? 2 : 1);
+    }
+    fence_mbar_init();
+    if (lane == 0) abort_s = 0;
   }
   int b, pos;
   bool bad_row;
   paged_row(p.s, row, &b, &pos, &bad_row);
   const int n_keys = max(pos + 1, 0);
   if (bad_row && threadIdx.x == 0 && p.status) atomicOr(p.status, kStatusBadIndex);
-
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::V_SLOTS; ++i) {
-      mbar_init(smem_u32(&v_full[i]), C::GATHER);
-      mbar_init(smem_u32(&v_empty[i]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&x_free[i]), 2);
-      mbar_init(smem_u32(&p_full[i]), 2);
-      mbar_init(smem_u32(&p_empty[i]), 2);
-      mbar_init(smem_u32(&o_ok[i]), 1);
-      mbar_init(smem_u32(&pv_done[i]), 1);
-      mbar_init(smem_u32(&mma_fin[i]), 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_u32(&x_full[i]), 1);
-      mbar_init(smem_u32(&m_full[i]), 1);
-    }
-    mbar_init(smem_u32(r_full), C::GATHER);
-    mbar_init(smem_u32(r_empty), 1);
-    mbar_init(smem_u32(&s_full[0]), 1);
-    mbar_init(smem_u32(&s_full[1]), 1);
-    mbar_init(smem_u32(s_empty), 4);
-    mbar_init(smem_u32(q_bar), 1);
-    abort_s = 0;
-    fence_mbar_init();
-  }
-  if (warp == 1) tmem_alloc(smem_u32(bars + 36), C::TMEM_COLS);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    // ---- Q: the rotary block and the CTA's value blocks into the (still idle) ring, h rows a block
-    // (lanes past h hold whatever was there and are never written out)
-    const uint32_t kb_bytes = static_cast<uint32_t>(p.h) * 128u;
-    tma_prefetch_desc(&q_map);
-    mbar_arrive_expect_tx(smem_u32(q_bar), (C::VKB + 1) * kb_bytes);
-    for (int j = 0; j <= C::VKB; ++j)
-      tma_load_2d(smem_u32(sV + j * C::Q_KB_BYTES), &q_map, smem_u32(q_bar),
-                  (j == 0 ? C::KB_ALL - 1 : c * C::VKB + j - 1) * 128, r * p.h);
-  }
   bool bad_idx = false;
   if (warp >= 8 && !dense) {
-    // ---- every selected key -> physical row (or -1), all block-table loads in flight together
-    int64_t phys[KPT];
+    // ---- every selected key -> physical row (or -1), all block-table loads in flight together;
+    // per tile the valid-key mask; invalid keys borrow the tile's first valid row
+    int32_t phys[2 * TPW];
 #pragma unroll
-    for (int j = 0; j < KPT; ++j) {
+    for (int j = 0; j < 2 * TPW; ++j) {
       phys[j] = -1;
-      if (v[j] >= 0 && v[j] < n_keys)
-        phys[j] = paged_phys(p.s, b, v[j]);
+      if (v[j] >= 0 && v[j] < n_keys) phys[j] = static_cast<int32_t>(paged_phys(p.s, b, v[j]));
       bad_idx |= v[j] >= 0 && phys[j] < 0;
     }
 #pragma unroll
-    for (int j = 0; j < KPT; ++j) {
-      const int e = static_cast<int>(threadIdx.x) - 256 + 256 * j;
-      if (e < p.topk) sPhys[e] = static_cast<int32_t>(phys[j]);
-    }
-  }
-  __syncthreads();
-  if (warp >= 8 && !dense) {
-    // ---- per tile: the valid-key mask; invalid keys borrow the tile's first valid row
-    for (int tt = warp - 8; tt < n_tiles_all; tt += 8) {
-      int32_t* ph = sPhys + tt * C::BN;
-      const int32_t a0 = ph[lane], a1 = ph[32 + lane];
-      const uint32_t lo = __ballot_sync(0xffffffffu, a0 >= 0);
-      const uint32_t hi = __ballot_sync(0xffffffffu, a1 >= 0);
-      const uint64_t m = (static_cast<uint64_t>(hi) << 32) | lo;
-      if (m != 0) {
-        const int32_t fb = ph[__ffsll(static_cast<long long>(m)) - 1];
-        __syncwarp();
-        if (a0 < 0) ph[lane] = fb;
-        if (a1 < 0) ph[32 + lane] = fb;
+    for (int j = 0; j < TPW; ++j) {
+      const int tt = warp - 8 + 8 * j;
+      const uint32_t lo = __ballot_sync(0xffffffffu, phys[2 * j] >= 0);
+      const uint32_t hi = __ballot_sync(0xffffffffu, phys[2 * j + 1] >= 0);
+      const int32_t first = __shfl_sync(0xffffffffu, lo != 0 ? phys[2 * j] : phys[2 * j + 1],
+                                        max(__ffs(lo != 0 ? lo : hi) - 1, 0));
+      if (tt < n_tiles_all) {
+        sPhys[tt * C::BN + lane] = phys[2 * j] >= 0 ? phys[2 * j] : first;
+        sPhys[tt * C::BN + 32 + lane] = phys[2 * j + 1] >= 0 ? phys[2 * j + 1] : first;
+        if (lane == 0) sMask[tt] = (static_cast<uint64_t>(hi) << 32) | lo;
       }
-      if (lane == 0) sMask[tt] = m;
     }
   }
   if (warp == 8 && dense) {
@@ -345,17 +324,18 @@ __global__ void __launch_bounds__(512, 1)
   }
   if (bad_idx && p.status) atomicOr(p.status, kStatusBadIndex);
   __syncthreads();
-  if (warp == 0 && lane == 0 && !dense) {
+  if (warp == 0 && !dense) {
     // ---- the active tiles of this split, identical in both CTAs of the row
-    int cnt = 0;
-    for (int t = 0; t < n_tiles_all; ++t)
-      if (sMask[t] != 0) sTiles[cnt++] = t;
+    const bool active = lane < n_tiles_all && sMask[lane] != 0;
+    const uint32_t act = __ballot_sync(0xffffffffu, active);
+    const int cnt = __popc(act), at = __popc(act & ((1u << lane) - 1u));
     const int per = (cnt + p.splits - 1) / p.splits;
     const int t0 = min(cnt, split * per);
     const int t1 = min(cnt, t0 + per);
-    for (int i = t0; i < t1; ++i) sTiles[i - t0] = sTiles[i];
-    n_act_s = t1 - t0;
+    if (active && at >= t0 && at < t1) sTiles[at - t0] = lane;
+    if (lane == 0) n_act_s = t1 - t0;
   }
+  __syncthreads();
   if (warp >= 4 && warp < 8) {
     // ---- Q from the staging area into TMEM: head = lane, two dims a column
     const int hrow = (warp & 3) * 32 + lane;
@@ -366,7 +346,7 @@ __global__ void __launch_bounds__(512, 1)
     } else {
       for (int kb = 0; kb <= C::VKB; ++kb) {
         uint32_t u[32];
-        const uint8_t* src = sV + kb * C::Q_KB_BYTES;
+        const uint8_t* src = sQ + kb * C::Q_KB_BYTES;
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) {
           const uint4 q4 = *reinterpret_cast<const uint4*>(src + sw128_offset(hrow, ch));
@@ -382,10 +362,14 @@ __global__ void __launch_bounds__(512, 1)
   }
   tc_fence_before();
   __syncwarp();
-  cluster_sync();   // the staging area is free for the ring, both CTAs' barriers are ready
+  // Behind this barrier the staging area is free for the ring and both CTAs' barriers are ready.  The
+  // gathering warps fill the first PRE_TILES slots, which the staging area leaves free, before they
+  // wait for it.
+  cluster_arrive();
+  if (warp < 8) cluster_wait();
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
-  const int n = abort_s ? 0 : n_act_s;
+  const int n = warp < 8 && abort_s ? 0 : n_act_s;
   auto mask_of = [&](int i) -> uint64_t {
     if (dense) return i == n - 1 ? sMask[0] : ~0ull;
     return sMask[sTiles[i]];
@@ -547,12 +531,17 @@ __global__ void __launch_bounds__(512, 1)
             q8_expand8(make_uint2(x.code[ks].z, x.code[ks].w), x.scale[ks / 2]);
       }
     };
-    bool ok = true;
+    bool ok = true, joined = false;
     int vs = 0;
     uint32_t vph = 1;                            // (the first use of each slot does not wait)
     // tile i (physical rows `rows`): its slots waited for, filled, and the barriers told; the set x
     // is then loaded with tile i + 2 (rows `rows2`)
     auto fill = [&](CodeSet& x, int i, int32_t rows, int32_t rows2) -> bool {
+      if (i == C::PRE_TILES) {                   // from here on the slots were Q's staging area
+        cluster_wait();
+        joined = true;
+        if (abort_s) return false;
+      }
       const uint8_t* const src[2] = {row_ptr(rows, rsub), row_ptr(rows, rsub + 4)};
       if ((i & 1) == c) {                        // the rotary block, on this CTA's tiles
         if (i >= 2 && !warp_wait(smem_u32(r_empty), ((i >> 1) - 1) & 1)) return false;
@@ -597,6 +586,7 @@ __global__ void __launch_bounds__(512, 1)
       abort_s = 1;
       if (p.status) atomicOr(p.status, kStatusTimeout);
     }
+    if (!joined) cluster_wait();
     cp_async_wait_all();   // nothing may still be writing this CTA's shared memory at exit
   } else if (!own) {
     // ------------------------------------------------------------ partial logits to their owner
@@ -806,42 +796,53 @@ __global__ void __launch_bounds__(512, 1)
   cluster_sync();      // both CTAs are done; nothing remote is touched after this
   {
     // ------------------------------------------------------------ epilogue: O / sum
+    // The rows are put together in the idle ring (at a pitch of 16 bytes more than a row, so that
+    // 8 lanes' 16-byte stores meet all banks) and leave as one bulk copy each.  Stored from the
+    // registers, a lane a row, a warp's 16-byte pieces touch 32 rows: 6800 cycles a CTA instead of
+    // TBD.
     const int hrow = q * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    const int64_t orow = static_cast<int64_t>(row) * p.h + hrow;
-    const int64_t prow = (static_cast<int64_t>(split) * p.row_count + r) * p.h + hrow;
-    float* po = p.part_o != nullptr ? p.part_o + prow * D_V + c * C::V_HALF : nullptr;
+    const bool part = p.part_o != nullptr;
+    const uint32_t row_bytes = C::V_HALF * (part ? 4 : 2);
+    const uint32_t stage = smem_u32(sV) + hrow * (row_bytes + 16);
     const float inv = sInv[hrow];
     for (int c0 = (warp >> 2) * 32; c0 < C::V_HALF; c0 += 128) {
-      float o[32];
-      if (n > 0) {                                // (uniform: the TMEM load is collective)
-        uint32_t u[32];
-        tmem_ld32(lane_addr + c0, u);
-        tmem_wait_ld();
+      uint32_t u[32];
+      tmem_ld32(lane_addr + c0, u);
+      tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = inv != 0.f ? __uint_as_float(u[j]) * inv : 0.f;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = 0.f;
-      }
-      if (hrow >= p.h) continue;
-      if (po != nullptr) {
+      for (int j = 0; j < 32; ++j)                // (a row without keys: 0, whatever TMEM holds)
+        u[j] = inv != 0.f ? __float_as_uint(__uint_as_float(u[j]) * inv) : 0u;
+      if (part) {
 #pragma unroll
         for (int j = 0; j < 32; j += 4)
-          *reinterpret_cast<float4*>(po + c0 + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          st_shared_v4(stage + (c0 + j) * 4, u[j], u[j + 1], u[j + 2], u[j + 3]);
       } else {
-        __nv_bfloat16* dst = p.out + orow * D_V + c * C::V_HALF + c0;
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
           uint32_t pk[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 two = __floats2bfloat162_rn(o[j + 2 * e], o[j + 2 * e + 1]);
+            const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(u[j + 2 * e]),
+                                                             __uint_as_float(u[j + 2 * e + 1]));
             pk[e] = *reinterpret_cast<const uint32_t*>(&two);
           }
-          *reinterpret_cast<uint4*>(dst + j) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          st_shared_v4(stage + (c0 + j) * 2, pk[0], pk[1], pk[2], pk[3]);
         }
       }
+    }
+    fence_proxy_async_smem();                     // the rows, before the copies read them
+    named_bar_sync(1 + q, 128);                   // the four warps of this quarter
+    if (warp < 4) {
+      if (hrow < p.h) {
+        const int64_t orow = static_cast<int64_t>(row) * p.h + hrow;
+        const int64_t prow = (static_cast<int64_t>(split) * p.row_count + r) * p.h + hrow;
+        void* dst = part ? static_cast<void*>(p.part_o + prow * D_V + c * C::V_HALF)
+                         : static_cast<void*>(p.out + orow * D_V + c * C::V_HALF);
+        bulk_store_s2g(dst, stage, row_bytes);
+      }
+      bulk_commit();
+      bulk_wait_read_all();
     }
   }
   tc_fence_before();

@@ -216,6 +216,14 @@ __device__ __forceinline__ void cluster_sync() {
                ::: "memory");
 }
 
+// The two halves of cluster_sync (every warp of the cluster does both, whole and in this order).
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Map a local shared address to the same offset in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -272,6 +280,13 @@ __device__ __forceinline__ void cp_async_wait_all() {
 __device__ __forceinline__ void bulk_reduce_add_f32(void* gdst, uint32_t ssrc, uint32_t bytes) {
   asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;"
                ::"l"(gdst), "r"(ssrc), "r"(bytes)
+               : "memory");
+}
+// Copies `bytes` (a multiple of 16) of this CTA's shared memory to global memory, both addresses
+// 16-byte aligned; completion is tracked per thread with bulk groups.
+__device__ __forceinline__ void bulk_store_s2g(void* gdst, uint32_t ssrc, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst), "r"(ssrc),
+               "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void bulk_commit() {
