@@ -833,7 +833,7 @@ __global__ void __launch_bounds__(512, 1)
     }
     fence_proxy_async_smem();                     // the rows, before the copies read them
     named_bar_sync(1 + q, 128);                   // the four warps of this quarter
-    if (warp < 4) {
+    if ((lane >> 3) == (warp >> 2)) {             // 8 rows a warp: a copy takes 67 cycles to issue
       if (hrow < p.h) {
         const int64_t orow = static_cast<int64_t>(row) * p.h + hrow;
         const int64_t prow = (static_cast<int64_t>(split) * p.row_count + r) * p.h + hrow;
