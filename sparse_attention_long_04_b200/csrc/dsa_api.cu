@@ -549,7 +549,12 @@ size_t mla_ws_bytes(const dsa_dims_t& d, int splits, int32_t row_count) {
   return size_t(splits) * row_count * d.h * (d.d_v + 1) * sizeof(float) + 256;
 }
 
-// Split-KV slices per row of the paged attention, chosen as mla_splits below chooses them.
+// Split-KV slices per row of the paged attention: the smallest estimated time in units of a tile
+// (1.1 us).  A CTA pair costs its tiles and some 10 more (indices, Q, filling and draining the
+// pipeline, output), combining costs 2 and 0.05 a row and split (its traffic).  Measured at
+// 2048 keys over 8-bit rows: 1 row, 4 / 8 / 16 splits: 23.7 / 19.5 / 18.0 us; 16 rows, 1 / 2 / 4:
+// 50.0 / 35.9 / 27.0; 32 rows, 1 / 2: 52.0 / 42.4; 80 rows, 1 / 2: 123 / 125; 100 rows, 1 / 2:
+// 127 / 132.
 int paged_splits(const dsa_dims_t& d, const dsa_seqs_t& s, int32_t row_count, int sm_count,
                  size_t max_ws = SIZE_MAX) {
   if (s.mode == DSA_PREFILL || row_count <= 0) return 1;
@@ -557,10 +562,11 @@ int paged_splits(const dsa_dims_t& d, const dsa_seqs_t& s, int32_t row_count, in
   const int sms = std::max(1, sm_count);
   int best = 1;
   double best_t = 1e30;
-  for (int sp = 1; sp <= std::min(16, std::max(1, tiles / 4)); ++sp) {
+  for (int sp = 1; sp <= std::min(kMaxPagedSplits, tiles); ++sp) {
     if (mla_ws_bytes(d, sp, row_count) > max_ws) continue;
     const double waves = std::ceil(2.0 * row_count * sp / sms);
-    const double t = waves * (3.0 + std::ceil(double(tiles) / sp)) + (sp > 1 ? 2.0 : 0.0);
+    const double t = waves * (10.0 + std::ceil(double(tiles) / sp)) +
+                     (sp > 1 ? 2.0 + 0.05 * row_count * sp : 0.0);
     if (t < best_t - 1e-9) {
       best_t = t;
       best = sp;
@@ -702,8 +708,10 @@ dsa_status_t paged_mla_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint
                           prm) != DSA_OK)
     return DSA_ERR_CUDA;
   if (splits > 1) {
-    dsa_paged_combine_kernel<D_V><<<dim3(row_count, d.h), D_V / 4, 0, st>>>(prm);
-    return launch_status();
+    // (few splits: fewer registers, so that more rows and heads are in flight)
+    return launch_pdl(splits <= 4 ? dsa_paged_combine_kernel<D_V, 4>
+                                  : dsa_paged_combine_kernel<D_V, kMaxPagedSplits>,
+                      dim3(row_count, d.h), D_V / 4, 0, st, prm);
   }
   return DSA_OK;
 }

@@ -61,6 +61,7 @@ struct PagedMlaParams {
 };
 
 constexpr int kMaxDenseTiles = 2048;   // tiles of one split without idx
+constexpr int kMaxPagedSplits = 16;    // splits of a row's tiles
 
 // Asynchronous stores into a CTA of the cluster (addr and bar are shared::cluster addresses of
 // that CTA); the bytes are counted on its barrier when they have landed.
@@ -215,6 +216,7 @@ __global__ void __launch_bounds__(512, 1)
   static_assert(kMaxDenseTiles <= C::MAX_TILES * C::BN, "dense tiles fit the key array");
 
   wait_prior_grid();   // (launched early: the indices come from the previous kernel)
+  if (p.part_o != nullptr) allow_next_grid();   // the combining kernel
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int c = static_cast<int>(cluster_ctarank());   // value half, and the heads it owns
   const uint32_t peer = static_cast<uint32_t>(c ^ 1);
@@ -799,7 +801,7 @@ __global__ void __launch_bounds__(512, 1)
     // The rows are put together in the idle ring (at a pitch of 16 bytes more than a row, so that
     // 8 lanes' 16-byte stores meet all banks) and leave as one bulk copy each.  Stored from the
     // registers, a lane a row, a warp's 16-byte pieces touch 32 rows: 6800 cycles a CTA instead of
-    // TBD.
+    // 2400.
     const int hrow = q * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const bool part = p.part_o != nullptr;
@@ -854,25 +856,38 @@ __global__ void __launch_bounds__(512, 1)
 }
 
 // Merge the splits' partials by their LSE: O = sum_i e^(LSE_i - LSE) O_i, LSE = log sum e^LSE_i.
-// One CTA per (row, head); a NaN partial makes the head NaN.
-template <int D_V>
+// One CTA per (row, head); a NaN partial makes the head NaN.  Launched while the attention kernel
+// runs, and every load is on its way before the first is used: one token over 2048 keys in 8
+// splits takes 19.5 us with the attention, 21.5 with a plain launch and the loads in loops.
+template <int D_V, int MAX_SPLITS>
 __global__ void __launch_bounds__(D_V / 4) dsa_paged_combine_kernel(const PagedMlaParams p) {
+  wait_prior_grid();
   const int r = blockIdx.x, hrow = blockIdx.y;
   const int64_t stride = static_cast<int64_t>(p.row_count) * p.h;
   const int64_t base = static_cast<int64_t>(r) * p.h + hrow;
-  float m = -INFINITY, wsum = 0.f;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.part_lse[s * stride + base]);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const int d = threadIdx.x * 4;
-  for (int s = 0; s < p.splits; ++s) {
-    const float lse = p.part_lse[s * stride + base];
-    const float w = lse == -INFINITY ? 0.f : expf(lse - m);   // a NaN LSE stays NaN
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (s * stride + base) * D_V + d);
+  float lse[MAX_SPLITS];
+  float4 v[MAX_SPLITS];
+#pragma unroll
+  for (int s = 0; s < MAX_SPLITS; ++s) {
+    const bool in = s < p.splits;
+    lse[s] = in ? p.part_lse[s * stride + base] : -INFINITY;
+    v[s] = in ? *reinterpret_cast<const float4*>(p.part_o + (s * stride + base) * D_V + d)
+              : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  float m = -INFINITY, wsum = 0.f;
+#pragma unroll
+  for (int s = 0; s < MAX_SPLITS; ++s) m = fmaxf(m, lse[s]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int s = 0; s < MAX_SPLITS; ++s) {
+    if (s >= p.splits) break;
+    const float w = lse[s] == -INFINITY ? 0.f : expf(lse[s] - m);   // a NaN LSE stays NaN
     wsum += w;
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
+    acc.x = fmaf(w, v[s].x, acc.x);
+    acc.y = fmaf(w, v[s].y, acc.y);
+    acc.z = fmaf(w, v[s].z, acc.z);
+    acc.w = fmaf(w, v[s].w, acc.w);
   }
   const bool any = !(wsum <= 0.f);
   const float inv = any ? 1.f / wsum : 0.f;

@@ -216,6 +216,12 @@ __device__ __forceinline__ void cluster_sync() {
                ::: "memory");
 }
 
+// Lets the next kernel of the stream, if it was launched with programmatic serialization, start once
+// every CTA of this one has come here (it then waits in wait_prior_grid for this one's completion).
+__device__ __forceinline__ void allow_next_grid() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // The two halves of cluster_sync (every warp of the cluster does both, whole and in this order).
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
