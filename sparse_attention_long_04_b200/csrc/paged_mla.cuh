@@ -143,7 +143,7 @@ struct PagedCfg {
   // (the dynamic array starts on a 1024-byte boundary: the kernel has no static shared memory)
   static constexpr int BARS = 39;
   static constexpr int SMEM_USED = V_SLOTS * V_SLOT_BYTES + KB_BYTES + 2 * P_BYTES + X_BYTES +
-                                   MAX_TILES * BN * 4 + MAX_TILES * 12 + 4 * 64 * 4 + BARS * 8;
+                                   MAX_TILES * BN * 4 + MAX_TILES * 12 + 8 * 64 * 4 + BARS * 8;
   // at least 116 KB, so that one CTA runs per SM (its TMEM allocation never waits)
   static constexpr int SMEM_BYTES = SMEM_USED > 116 * 1024 ? SMEM_USED : 116 * 1024;
   static_assert(V_HALF % 64 == 0 && V_HALF <= 256, "PV MMA N");
@@ -191,10 +191,11 @@ __global__ void __launch_bounds__(512, 1)
   int32_t* sTiles = reinterpret_cast<int32_t*>(sMask + C::MAX_TILES);            // [32]
   float* sAlpha = reinterpret_cast<float*>(sTiles + C::MAX_TILES);   // [2][64] from the partner
   float* sRef = sAlpha + 2 * 64;                  // [2][64 heads] the reference after a tile
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sRef + 2 * 64);
-  // after the last tile, over the rows that no one reads any more:
-  float* sSum = reinterpret_cast<float*>(sPhys);  // [2 warps][sum, reference][64 heads]
-  float* sInv = sSum + 4 * 64;                    // [128] 1 / sum
+  float* sSum = sRef + 2 * 64;                    // [2 warps][sum, reference][64 heads]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sSum + 4 * 64);
+  // after the last tile, over the rows that no one reads any more (sSum is not: with one tile a
+  // softmax warp has none and writes its sums at once)
+  float* sInv = reinterpret_cast<float*>(sPhys);  // [128] 1 / sum
   uint64_t* v_full = bars;           // [5] every gathering thread
   uint64_t* v_empty = bars + 5;      // [5] PV commit
   uint64_t* r_full = bars + 10;      // every gathering thread (rotary copies landed)

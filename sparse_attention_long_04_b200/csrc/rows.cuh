@@ -29,7 +29,8 @@ __device__ __forceinline__ int seq_of_row(const int32_t* cu, int batch, int row)
 }
 
 // Sequence of `row` and its position; a context above max_seqlen (a caller error) is taken as
-// max_seqlen and *bad set.  A position below 0 (more new tokens than context) has no keys.
+// max_seqlen and *bad set.  A position below 0 (more new tokens than context, or a row behind the
+// last sequence) has no keys.
 __device__ __forceinline__ void paged_row(const PagedSeqs& s, int row, int* b, int* pos,
                                           bool* bad) {
   int len, ahead;
@@ -41,8 +42,8 @@ __device__ __forceinline__ void paged_row(const PagedSeqs& s, int row, int* b, i
     ahead = 1;
   }
   len = s.seq_lens[*b];
-  *bad = len > s.max_seqlen || len < ahead;
-  *pos = min(len, s.max_seqlen) - ahead;
+  *bad = len > s.max_seqlen || len < ahead || ahead < 1;
+  *pos = ahead < 1 ? -1 : min(len, s.max_seqlen) - ahead;
 }
 
 // Cache row of logical key `pos` of sequence b, -1 when its page lies outside the caches.

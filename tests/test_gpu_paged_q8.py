@@ -309,6 +309,87 @@ def test_attention_growing_logits(dsa, q8):
 
 
 @pytest.mark.parametrize("q8", [True, False], ids=["q8", "bf16"])
+@pytest.mark.parametrize("new,ctx", [([1], [1000]), ([200], [1000])], ids=["split", "whole"])
+def test_attention_one_tile(dsa, q8, new, ctx):
+    """One active tile a CTA pair, at every place of the selection: 16 splits of one tile each, and
+    rows whose only entries fill tile 0, 1, 2, ..."""
+    d = FULL
+    pg = Pages(new, ctx, seed=25)
+    pb = pg.problem(dsa, d, 1024)
+    cache, values = _cache(pg, d, q8, 201)
+    q = _queries(pg.rows, d, 202)
+    idx = torch.from_numpy(ref.random_selection(pg, 1024, 203)).cuda()
+    if pg.rows > 1:
+        tile = torch.arange(1024, device="cuda") // 64
+        only = tile[None, :] == (torch.arange(pg.rows, device="cuda") % 12)[:, None]
+        idx = torch.where(only, idx, -1)
+    out, lse, status = _attend(dsa, pb, q8, q, cache, idx, pg.rows)
+    assert status == 0
+    ref.check_attention_rows(out, lse, q, values, idx, pg, d["d_qk"] ** -0.5, d)
+    for _ in range(20):
+        again, lagain, _ = _attend(dsa, pb, q8, q, cache, idx, pg.rows)
+        assert torch.equal(again, out) and torch.equal(lagain, lse)
+
+
+@pytest.mark.parametrize("q8", [True, False], ids=["q8", "bf16"])
+@pytest.mark.parametrize("new", [[1], [160]], ids=["split", "whole"])
+def test_attention_minus_infinite_logits(dsa, q8, new):
+    """Selected keys whose logits are -inf (a rotary dim of -inf against a positive query) have
+    probability 0, a whole first tile of them included."""
+    d = FULL
+    pg = Pages(new, [600], seed=26)
+    pb = pg.problem(dsa, d, 256)
+    lat = ref.latents(pg.kv_rows, d, 211)
+    minus = np.arange(64)
+    lat[torch.as_tensor(pg.phys(0, minus), device="cuda"), d["d_v"]] = float("-inf")
+    if q8:
+        packed = ref.pack_rows(lat, d)
+        cache, values = torch.from_numpy(packed).cuda(), torch.from_numpy(
+            ref.unpack_rows(packed, d)).cuda()
+    else:
+        cache, values = lat, lat.double()
+    q = _queries(pg.rows, d, 212)
+    q[:, :, d["d_v"]] = 1.0
+    idx = torch.full((pg.rows, 256), -1, dtype=torch.int32, device="cuda")
+    idx[:, :64] = torch.arange(64, dtype=torch.int32)
+    idx[:, 64:256] = torch.arange(100, 292, dtype=torch.int32)
+    rest = idx.clone()
+    rest[:, :64] = -1
+    out, lse, status = _attend(dsa, pb, q8, q, cache, idx, pg.rows)
+    assert status == 0
+    ref.check_attention_rows(out, lse, q, values, rest, pg, d["d_qk"] ** -0.5, d)
+
+
+def test_rows_behind_the_last_sequence(dsa):
+    """Rows that the device's cu_seqlens gives to no sequence see no keys and are reported; the
+    tokens of such rows are not written."""
+    d = FULL
+    pg = Pages([3, 4], [70, 300], seed=27)
+    pb = pg.problem(dsa, d, 128)
+    cache, values = _cache(pg, d, True, 221)
+    q = _queries(pg.rows, d, 222)
+    idx = torch.from_numpy(ref.random_selection(pg, 128, 223)).cuda()
+    out, lse, status = _attend(dsa, pb, True, q, cache, idx, pg.rows)
+    assert status == 0
+    pg.d_cu[2] = 5                                   # sequence 1 keeps two of its four new tokens
+    pg.d_ctx[1] = 298
+    o2, l2, status = _attend(dsa, pb, True, q, cache, idx, pg.rows)
+    assert status == dsa.DSA_DEVICE_BAD_INDEX
+    assert torch.equal(o2[:5], out[:5]) and torch.equal(l2[:5], lse[:5])
+    assert (o2[5:] == 0).all() and (l2[5:] == float("-inf")).all()
+    k_new, kv_new = _new_tokens(pg.rows, d, 224)
+    k8 = torch.zeros(pg.kv_rows, 128, dtype=torch.uint8, device="cuda")
+    ks = torch.zeros(pg.kv_rows, device="cuda")
+    before = cache.clone()
+    st = _status()
+    assert dsa.dsa_cache_append_q8(pb, k_new, kv_new, k8, ks, cache, st) == dsa.DSA_OK
+    assert int(st.item()) == dsa.DSA_DEVICE_BAD_INDEX
+    changed = (cache != before).any(dim=1).nonzero().flatten().cpu().numpy()
+    places = np.concatenate([pg.phys(0, np.arange(67, 70)), pg.phys(1, np.arange(296, 298))])
+    assert sorted(changed) == sorted(places)
+
+
+@pytest.mark.parametrize("q8", [True, False], ids=["q8", "bf16"])
 def test_attention_ignores_unselected_nan(dsa, q8):
     """NaN and infinities in cache rows that no entry selects (and in unused pages) change
     nothing."""
