@@ -62,6 +62,14 @@ struct PagedMlaParams {
 
 constexpr int kMaxDenseTiles = 2048;   // tiles of one split without idx
 constexpr int kMaxPagedSplits = 16;    // splits of a row's tiles
+// Up to this many pages a sequence (131072 keys) its block-table row is copied to shared memory, one
+// coalesced trip, and the selected keys look their pages up there; looked up in global memory they
+// come 1600 cycles later, since each of a warp's 8 loads touches up to 32 sectors.
+constexpr int kStagedBlocks = 2048;
+// Named barriers (1-4: the output's quarters).  kSetupBar: warps 0-7, behind the set-up; kGatherBar:
+// warps 8-15, behind the staged table; kReadyBar: warps 8-15 wait for the set-up and for one
+// another's keys; kKeysBar: warps 0-7 wait for the keys, having copied Q.
+constexpr uint32_t kSetupBar = 5, kGatherBar = 6, kReadyBar = 7, kKeysBar = 8;
 
 // Asynchronous stores into a CTA of the cluster (addr and bar are shared::cluster addresses of
 // that CTA); the bytes are counted on its barrier when they have landed.
@@ -263,72 +271,139 @@ __global__ void __launch_bounds__(512, 1)
     fence_mbar_init();
     if (lane == 0) abort_s = 0;
   }
-  int b, pos;
-  bool bad_row;
-  paged_row(p.s, row, &b, &pos, &bad_row);
-  const int n_keys = max(pos + 1, 0);
-  if (bad_row && threadIdx.x == 0 && p.status) atomicOr(p.status, kStatusBadIndex);
   bool bad_idx = false;
-  if (warp >= 8 && !dense) {
-    // ---- every selected key -> physical row (or -1), all block-table loads in flight together;
-    // per tile the valid-key mask; invalid keys borrow the tile's first valid row
-    int32_t phys[2 * TPW];
+  if (warp < 8) {
+    named_bar_sync(kSetupBar, 256);
+    named_bar_arrive(kReadyBar, 512);
+    if (warp >= 4) {
+      // ---- Q from the staging area into TMEM: head = lane, two dims a column
+      const int hrow = (warp & 3) * 32 + lane;
+      const uint32_t lane_addr = tmem_base_s + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      if (!(warp_wait(smem_u32(q_bar), 0))) {
+        abort_s = 1;
+        if (p.status) atomicOr(p.status, kStatusTimeout);
+      } else {
+        for (int kb = 0; kb <= C::VKB; ++kb) {
+          uint32_t u[32];
+          const uint8_t* src = sQ + kb * C::Q_KB_BYTES;
 #pragma unroll
-    for (int j = 0; j < 2 * TPW; ++j) {
-      phys[j] = -1;
-      if (v[j] >= 0 && v[j] < n_keys) phys[j] = static_cast<int32_t>(paged_phys(p.s, b, v[j]));
-      bad_idx |= v[j] >= 0 && phys[j] < 0;
-    }
-#pragma unroll
-    for (int j = 0; j < TPW; ++j) {
-      const int tt = warp - 8 + 8 * j;
-      const uint32_t lo = __ballot_sync(0xffffffffu, phys[2 * j] >= 0);
-      const uint32_t hi = __ballot_sync(0xffffffffu, phys[2 * j + 1] >= 0);
-      const int32_t first = __shfl_sync(0xffffffffu, lo != 0 ? phys[2 * j] : phys[2 * j + 1],
-                                        max(__ffs(lo != 0 ? lo : hi) - 1, 0));
-      if (tt < n_tiles_all) {
-        sPhys[tt * C::BN + lane] = phys[2 * j] >= 0 ? phys[2 * j] : first;
-        sPhys[tt * C::BN + 32 + lane] = phys[2 * j + 1] >= 0 ? phys[2 * j + 1] : first;
-        if (lane == 0) sMask[tt] = (static_cast<uint64_t>(hi) << 32) | lo;
+          for (int ch = 0; ch < 8; ++ch) {
+            const uint4 q4 = *reinterpret_cast<const uint4*>(src + sw128_offset(hrow, ch));
+            u[4 * ch + 0] = q4.x;
+            u[4 * ch + 1] = q4.y;
+            u[4 * ch + 2] = q4.z;
+            u[4 * ch + 3] = q4.w;
+          }
+          tmem_st32(lane_addr + C::QR_COL + kb * 32, u);
+        }
+        tmem_wait_st();
       }
     }
-  }
-  if (warp == 8 && dense) {
-    // ---- this split's tiles (one page each) whose page is inside the cache, in key order;
-    // only the row's last tile can be partial
-    const int tiles = (n_keys + C::BN - 1) / C::BN;
-    const int per = (tiles + p.splits - 1) / p.splits;
-    const int t0 = min(tiles, split * per);
-    const int t1 = min(tiles, t0 + min(per, kMaxDenseTiles));
-    int cnt = 0;
-    bool tail = false;
-    for (int base = t0; base < t1; base += 32) {
-      const int t = base + lane;
-      int64_t ph = -1;
-      if (t < t1) {
-        ph = paged_phys(p.s, b, t * C::BN);
-        // every key of the tile that the row sees must be inside the cache
-        const int n = min(C::BN, n_keys - t * C::BN);
-        if (ph >= 0 && ph + n > p.s.num_kv_rows) ph = -1;
-        bad_idx |= ph < 0;
+    // Behind the cluster barrier the staging area is free for the ring and both CTAs' barriers are
+    // ready.  It is arrived at early (a releasing arrival waits some 2000 cycles for the warp's memory
+    // operations); the gathering warps fill the first PRE_TILES slots, which the staging area
+    // leaves free, before they wait for it.
+    tc_fence_before();
+    __syncwarp();
+    cluster_arrive();
+    named_bar_sync(kKeysBar, 512);
+  } else {
+    cluster_arrive_relaxed();
+    int b, pos;
+    bool bad_row;
+    paged_row(p.s, row, &b, &pos, &bad_row);
+    const int n_keys = max(pos + 1, 0);
+    if (bad_row && threadIdx.x == 256 && p.status) atomicOr(p.status, kStatusBadIndex);
+    if (!dense) {
+      // ---- every selected key -> physical row (or -1); per tile the valid-key mask; invalid keys
+      // borrow the tile's first valid row
+      int32_t* sTable = reinterpret_cast<int32_t*>(sP);     // (P comes later)
+      const int blocks = (p.s.max_seqlen + 63) / 64;
+      const bool staged = p.s.block_table != nullptr && blocks <= kStagedBlocks;
+      if (staged) {
+        const int32_t* table = p.s.block_table + static_cast<int64_t>(b) * p.s.max_blocks;
+        const int e0 = static_cast<int>(threadIdx.x) - 256;
+        int32_t t[kStagedBlocks / 256];
+#pragma unroll
+        for (int j = 0; j < kStagedBlocks / 256; ++j)
+          t[j] = e0 + 256 * j < blocks ? __ldg(table + e0 + 256 * j) : -1;
+#pragma unroll
+        for (int j = 0; j < kStagedBlocks / 256; ++j)
+          if (e0 + 256 * j < blocks) sTable[e0 + 256 * j] = t[j];
+        named_bar_sync(kGatherBar, 256);
       }
-      const uint32_t good = __ballot_sync(0xffffffffu, ph >= 0);
-      if (ph >= 0) sPhys[cnt + __popc(good & ((1u << lane) - 1u))] = static_cast<int32_t>(ph);
-      cnt += __popc(good);
-      const int last = tiles - 1 - base;
-      if (last >= 0 && last < 32) tail = (good >> last) & 1u;
+      int32_t phys[2 * TPW];
+      if (staged) {                               // (no branches: all lookups at once)
+#pragma unroll
+        for (int j = 0; j < 2 * TPW; ++j) {
+          const bool in = v[j] >= 0 && v[j] < n_keys;
+          const int64_t at = static_cast<int64_t>(sTable[in ? v[j] >> 6 : 0]) * 64 + (v[j] & 63);
+          phys[j] = in && at >= 0 && at < p.s.num_kv_rows ? static_cast<int32_t>(at) : -1;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2 * TPW; ++j)
+          phys[j] = v[j] >= 0 && v[j] < n_keys
+                        ? static_cast<int32_t>(paged_phys(p.s, b, v[j])) : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < 2 * TPW; ++j) bad_idx |= v[j] >= 0 && phys[j] < 0;
+#pragma unroll
+      for (int j = 0; j < TPW; ++j) {
+        const int tt = warp - 8 + 8 * j;
+        const uint32_t lo = __ballot_sync(0xffffffffu, phys[2 * j] >= 0);
+        const uint32_t hi = __ballot_sync(0xffffffffu, phys[2 * j + 1] >= 0);
+        const int32_t first = __shfl_sync(0xffffffffu, lo != 0 ? phys[2 * j] : phys[2 * j + 1],
+                                          max(__ffs(lo != 0 ? lo : hi) - 1, 0));
+        if (tt < n_tiles_all) {
+          sPhys[tt * C::BN + lane] = phys[2 * j] >= 0 ? phys[2 * j] : first;
+          sPhys[tt * C::BN + 32 + lane] = phys[2 * j + 1] >= 0 ? phys[2 * j + 1] : first;
+          if (lane == 0) sMask[tt] = (static_cast<uint64_t>(hi) << 32) | lo;
+        }
+      }
     }
-    if (lane == 0) {
-      n_act_s = cnt;
-      const int rem = n_keys - (tiles - 1) * C::BN;    // keys of the row's last tile
-      // sMask[0]: the mask of the last active tile
-      sMask[0] = tail && rem < C::BN ? (1ull << rem) - 1ull : ~0ull;
+    if (dense && warp == 8) {
+      // ---- this split's tiles (one page each) whose page is inside the cache, in key order;
+      // only the row's last tile can be partial
+      const int tiles = (n_keys + C::BN - 1) / C::BN;
+      const int per = (tiles + p.splits - 1) / p.splits;
+      const int t0 = min(tiles, split * per);
+      const int t1 = min(tiles, t0 + min(per, kMaxDenseTiles));
+      int cnt = 0;
+      bool tail = false;
+      for (int base = t0; base < t1; base += 32) {
+        const int t = base + lane;
+        int64_t ph = -1;
+        if (t < t1) {
+          ph = paged_phys(p.s, b, t * C::BN);
+          // every key of the tile that the row sees must be inside the cache
+          const int n = min(C::BN, n_keys - t * C::BN);
+          if (ph >= 0 && ph + n > p.s.num_kv_rows) ph = -1;
+          bad_idx |= ph < 0;
+        }
+        const uint32_t good = __ballot_sync(0xffffffffu, ph >= 0);
+        if (ph >= 0) sPhys[cnt + __popc(good & ((1u << lane) - 1u))] = static_cast<int32_t>(ph);
+        cnt += __popc(good);
+        const int last = tiles - 1 - base;
+        if (last >= 0 && last < 32) tail = (good >> last) & 1u;
+      }
+      if (lane == 0) {
+        n_act_s = cnt;
+        const int rem = n_keys - (tiles - 1) * C::BN;    // keys of the row's last tile
+        // sMask[0]: the mask of the last active tile
+        sMask[0] = tail && rem < C::BN ? (1ull << rem) - 1ull : ~0ull;
+      }
     }
+    if (bad_idx && p.status) atomicOr(p.status, kStatusBadIndex);
+    named_bar_sync(kReadyBar, 512);
+    named_bar_arrive(kKeysBar, 512);
   }
-  if (bad_idx && p.status) atomicOr(p.status, kStatusBadIndex);
-  __syncthreads();
-  if (warp == 0 && !dense) {
-    // ---- the active tiles of this split, identical in both CTAs of the row
+  // ---- the active tiles of this split, identical in both CTAs of the row (every warp writes the
+  // same list, to read it without another barrier)
+  int n_act;
+  if (dense) {
+    n_act = n_act_s;
+  } else {
     const bool active = lane < n_tiles_all && sMask[lane] != 0;
     const uint32_t act = __ballot_sync(0xffffffffu, active);
     const int cnt = __popc(act), at = __popc(act & ((1u << lane) - 1u));
@@ -336,43 +411,13 @@ __global__ void __launch_bounds__(512, 1)
     const int t0 = min(cnt, split * per);
     const int t1 = min(cnt, t0 + per);
     if (active && at >= t0 && at < t1) sTiles[at - t0] = lane;
-    if (lane == 0) n_act_s = t1 - t0;
+    n_act = t1 - t0;
+    __syncwarp();
   }
-  __syncthreads();
-  if (warp >= 4 && warp < 8) {
-    // ---- Q from the staging area into TMEM: head = lane, two dims a column
-    const int hrow = (warp & 3) * 32 + lane;
-    const uint32_t lane_addr = tmem_base_s + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    if (!(warp_wait(smem_u32(q_bar), 0))) {
-      abort_s = 1;
-      if (p.status) atomicOr(p.status, kStatusTimeout);
-    } else {
-      for (int kb = 0; kb <= C::VKB; ++kb) {
-        uint32_t u[32];
-        const uint8_t* src = sQ + kb * C::Q_KB_BYTES;
-#pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {
-          const uint4 q4 = *reinterpret_cast<const uint4*>(src + sw128_offset(hrow, ch));
-          u[4 * ch + 0] = q4.x;
-          u[4 * ch + 1] = q4.y;
-          u[4 * ch + 2] = q4.z;
-          u[4 * ch + 3] = q4.w;
-        }
-        tmem_st32(lane_addr + C::QR_COL + kb * 32, u);
-      }
-      tmem_wait_st();
-    }
-  }
-  tc_fence_before();
-  __syncwarp();
-  // Behind this barrier the staging area is free for the ring and both CTAs' barriers are ready.  The
-  // gathering warps fill the first PRE_TILES slots, which the staging area leaves free, before they
-  // wait for it.
-  cluster_arrive();
   if (warp < 8) cluster_wait();
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
-  const int n = warp < 8 && abort_s ? 0 : n_act_s;
+  const int n = warp < 8 && abort_s ? 0 : n_act;
   auto mask_of = [&](int i) -> uint64_t {
     if (dense) return i == n - 1 ? sMask[0] : ~0ull;
     return sMask[sTiles[i]];

@@ -28,14 +28,29 @@ __device__ __forceinline__ int seq_of_row(const int32_t* cu, int batch, int row)
   return lo;
 }
 
-// Sequence of `row` and its position; a context above max_seqlen (a caller error) is taken as
+// The same for a row that every lane of a (converged) warp asks for: 32 sequences a step instead of
+// one, since each step is a trip to L2.
+__device__ __forceinline__ int seq_of_warp_row(const int32_t* cu, int batch, int row) {
+  const int lane = static_cast<int>(threadIdx.x & 31u);
+  int lo = 0, n = batch;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const bool at = lane * step < n && cu[lo + lane * step] <= row;
+    const int k = max(__popc(__ballot_sync(0xffffffffu, at)) - 1, 0);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
+// Sequence of `row`, the same in all lanes of a converged warp, and its position; a context above max_seqlen (a caller error) is taken as
 // max_seqlen and *bad set.  A position below 0 (more new tokens than context, or a row behind the
 // last sequence) has no keys.
 __device__ __forceinline__ void paged_row(const PagedSeqs& s, int row, int* b, int* pos,
                                           bool* bad) {
   int len, ahead;
   if (s.chunk) {
-    *b = seq_of_row(s.cu_seqlens, s.batch, row);
+    *b = seq_of_warp_row(s.cu_seqlens, s.batch, row);
     ahead = s.cu_seqlens[*b + 1] - row;            // this row and the new tokens behind it
   } else {
     *b = row;
