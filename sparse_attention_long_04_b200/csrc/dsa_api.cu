@@ -673,7 +673,7 @@ dsa_status_t paged_mla_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint
                             const void* kv, const int32_t* idx, int32_t row_begin,
                             int32_t row_count, uint16_t* out, float* lse, void* ws,
                             size_t ws_bytes, int32_t* status, cudaStream_t st, int splits) {
-  using C = PagedCfg<D_QK, D_V>;
+  using C = PagedCfg<D_QK, D_V, kQ8>;
   PagedMlaParams prm{};
   prm.s = paged_seqs(s);
   prm.kv = static_cast<const uint8_t*>(kv);

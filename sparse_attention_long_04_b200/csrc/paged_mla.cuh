@@ -16,16 +16,20 @@
 // to its partner, counted in bytes on the receiver's barriers.
 //
 // Both CTAs gathering whole keys and computing all logits instead (nothing exchanged): 592 rows x
-// 2048 keys of (576, 512) take 408 us from the bf16 cache and 496 us from the 8-bit one, against 395
-// and 436 here.  There the shared-memory pipe is the limit (bf16 rows 98% busy: 36 KB of copies in
-// and 64 + 72 KB of MMA operands a tile out); here it is the chain of a tile's exchange and softmax,
-// some 4200 cycles with two tiles in flight.
+// 2048 keys of (576, 512) take 408 us from the bf16 cache and 496 us from the 8-bit one, against 349
+// and 398 here.  There the shared-memory pipe is the limit (bf16 rows 98% busy: 36 KB of copies in
+// and 64 + 72 KB of MMA operands a tile out).  Here no pipe is above 56%: a tile takes some 2050
+// cycles because a softmax warp's chain of waits, from a tile's product to its probabilities, is
+// 3500-4000 with two warps a quarter in turn, and 15% of a CTA's time is its fixed cost (indices, Q,
+// filling, draining, output).  Sending the logits by bulk copies, a second logit buffer, the QK
+// issuer freed of the rescaling: each as slow or slower (398 -> 411, 404, 391 with 5 slots but
+// bf16 349 -> 382).
 //
 // Tensor work of a tile at (576, 512): 16 or 20 QK MMAs of N = 64 (32 cycles each, A in TMEM) and
-// 4 PV MMAs of N = 256 (128 cycles): 1090 cycles on average of the some 1950 a tile takes.  The
-// MMAs are issued by one elected lane of a converged warp (elect.sync) from precomputed
-// descriptors: issued from an ordinary `lane == 0` branch with the descriptors built on the way,
-// one costs 76-90 cycles whatever its size.
+// 4 PV MMAs of N = 256 (128 cycles): 1090 cycles on average.  The MMAs are issued by one elected
+// lane of a converged warp (elect.sync) from precomputed descriptors: issued from an ordinary
+// `lane == 0` branch with the descriptors built on the way, one costs 76-90 cycles whatever its
+// size.
 //
 // 8-bit rows: the gather warps read the codes into registers, expand them to bf16 (exactly: the
 // scales are powers of two) and store them into the same swizzled tiles the bf16 gather fills
@@ -126,13 +130,16 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 // Tile sizes, rings and columns.
-template <int D_QK, int D_V>
+template <int D_QK, int D_V, bool kQ8>
 struct PagedCfg {
   static constexpr int KB_ALL = (D_QK + 63) / 64;     // 64-dim k-blocks of a latent row
   static constexpr int V_HALF = D_V / 2;              // value dims per CTA
   static constexpr int VKB = V_HALF / 64;             // value blocks per CTA
   static constexpr int BN = 64;                       // keys per tile
-  static constexpr int V_SLOTS = 5;                   // a slot is held from QK to PV, some 3 tiles
+  // A slot is held from QK to PV, some 3 tiles.  8-bit codes are loaded through L1, which gets what
+  // shared memory leaves: with 4 slots 64 tokens over 64 contexts (rows from HBM) take 59 us, with 5
+  // 66; 592 rows of one context (rows from L2) 398 and 392.  cp.async rows pass L1 by: 357 and 349.
+  static constexpr int V_SLOTS = kQ8 ? 4 : 5;
   static constexpr int MAX_TILES = 32;                // topk <= 2048
   static constexpr int THREADS = 512;
   static constexpr int GATHER = 256;                  // gathering threads
@@ -160,7 +167,8 @@ struct PagedCfg {
   static constexpr int Q_OFF = V_SLOTS * V_SLOT_BYTES - (VKB + 1) * Q_KB_BYTES;   // Q staging
   static constexpr int PRE_TILES = Q_OFF / V_SLOT_BYTES;      // slots in front of it
   static_assert(Q_OFF >= 0, "Q staging fits the ring");
-  static_assert(128 * (V_HALF * 4 + 16) <= V_SLOTS * V_SLOT_BYTES, "output staging fits the ring");
+  static_assert(128 * (V_HALF * 4 + 16) <= V_SLOTS * V_SLOT_BYTES + KB_BYTES,
+                "output staging fits the ring and the rotary block behind it");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -183,7 +191,7 @@ __device__ __forceinline__ void rescale_o(uint32_t addr, float alpha) {
 template <int D_QK, int D_V, bool kQ8>
 __global__ void __launch_bounds__(512, 1)
     dsa_paged_mla_kernel(const __grid_constant__ CUtensorMap q_map, const PagedMlaParams p) {
-  using C = PagedCfg<D_QK, D_V>;
+  using C = PagedCfg<D_QK, D_V, kQ8>;
   using R = Q8Row<D_QK, D_V>;
   constexpr int ROW_BYTES = kQ8 ? R::BYTES : D_QK * 2;
   static_assert(R::ROPE <= 64 && D_V % 128 == 0, "rotary dims fill (part of) the last k-block");
@@ -204,8 +212,8 @@ __global__ void __launch_bounds__(512, 1)
   // after the last tile, over the rows that no one reads any more (sSum is not: with one tile a
   // softmax warp has none and writes its sums at once)
   float* sInv = reinterpret_cast<float*>(sPhys);  // [128] 1 / sum
-  uint64_t* v_full = bars;           // [5] every gathering thread
-  uint64_t* v_empty = bars + 5;      // [5] PV commit
+  uint64_t* v_full = bars;           // [V_SLOTS] every gathering thread
+  uint64_t* v_empty = bars + 5;      // [V_SLOTS] PV commit
   uint64_t* r_full = bars + 10;      // every gathering thread (rotary copies landed)
   uint64_t* r_empty = bars + 11;     // QK commit of a rotary tile
   uint64_t* s_full = bars + 12;      // [2 tiles] QK commit
@@ -717,9 +725,21 @@ __global__ void __launch_bounds__(512, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(s_empty));
+      // (the waits that this tile's probabilities need are passed where the warp waits for the
+      // partner anyway: the other warp's references here, the P buffer between the key halves, when
+      // the partner may already send the next tile's first half.  Behind the maxima: 592 rows in
+      // 396 instead of 391 us from 8-bit rows, 362 instead of 349 from bf16.)
+      float m_old = -INFINITY;
+      if (i >= 1) {
+        ok = warp_wait(smem_u32(&m_full[(q & 1) * 2 + (t ^ 1)]), ((i - 1) >> 1) & 1);
+        if (!ok) break;
+        m_old = sRef[(t ^ 1) * 64 + hloc];
+      }
       // ---- plus the partner's half of these logits, 32 keys at a time
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        if (h == 1 && ok && i >= 2)                 // both PV(i - 2)
+          ok = warp_wait<true>(smem_u32(&p_empty[t]), ph ^ 1u);
         if (ok) ok = warp_wait<true>(xb + h * 8, ph);
         if (!ok) break;
 #pragma unroll
@@ -751,18 +771,10 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
       for (int e = 4; e < 32; ++e) mm[e & 3] = fmaxf(fmaxf(mm[e & 3], s[e].x), s[e].y);
       const float m_tile = fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * p.scale_log2;
-      float m_old = -INFINITY;
-      if (i >= 1) {
-        ok = warp_wait(smem_u32(&m_full[(q & 1) * 2 + (t ^ 1)]), ((i - 1) >> 1) & 1);
-        if (!ok) break;
-        m_old = sRef[(t ^ 1) * 64 + hloc];
-      }
       const float m_ref = head && m_tile > m_old + 8.0f ? m_tile : m_old;
       sRef[t * 64 + hloc] = m_ref;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&m_full[(q & 1) * 2 + t]));
-      if (i >= 2) ok = warp_wait<true>(smem_u32(&p_empty[t]), ph ^ 1u);   // both PV(i - 2)
-      if (!ok) break;
       // ---- p = 2^(sigma log2e s - reference) into shared memory, two keys to an instruction.  The
       // denominator sums the fp32 probabilities, only the PV operand is rounded (bf16: the MMA's
       // operand type).
