@@ -390,6 +390,46 @@ def test_rows_behind_the_last_sequence(dsa):
 
 
 @pytest.mark.parametrize("q8", [True, False], ids=["q8", "bf16"])
+def test_attention_wide_block_table(dsa, q8):
+    """A block table of more pages than are looked up in shared memory (max_seqlen past 131072)."""
+    d = FULL
+    pg = Pages([5, 1], [900, 70], seed=28, max_seqlen=140000)
+    pb = pg.problem(dsa, d, 512)
+    cache, values = _cache(pg, d, q8, 231)
+    q = _queries(pg.rows, d, 232)
+    idx = torch.from_numpy(ref.random_selection(pg, 512, 233, 0.2)).cuda()
+    out, lse, status = _attend(dsa, pb, q8, q, cache, idx, pg.rows)
+    assert status == 0
+    ref.check_attention_rows(out, lse, q, values, idx, pg, d["d_qk"] ** -0.5, d)
+
+
+def test_many_sequences(dsa):
+    """More than 32 x 32 sequences, some without new tokens: every row finds its own."""
+    d = FULL
+    new = [(0, 1, 2, 1)[i % 4] for i in range(1100)]
+    ctx = [n + i % 3 + (n == 0) for i, n in enumerate(new)]
+    pg = Pages(new, ctx, seed=29)
+    pb = pg.problem(dsa, d, 64)
+    cache, values = _cache(pg, d, True, 241)
+    k_new, kv_new = torch.randn(pg.rows, 128, device="cuda"), ref.latents(pg.rows, d, 242)
+    k8 = torch.zeros(pg.kv_rows, 128, dtype=torch.uint8, device="cuda")
+    ks = torch.zeros(pg.kv_rows, device="cuda")
+    status = _status()
+    assert dsa.dsa_cache_append_q8(pb, k_new, kv_new, k8, ks, cache, status) == dsa.DSA_OK
+    assert int(status.item()) == 0
+    want = ref.pack_rows(kv_new, d)
+    where = np.concatenate([pg.phys(*pg.row(r)).reshape(1) for r in range(pg.rows)])
+    assert np.array_equal(cache.cpu().numpy()[where], want)
+    values = torch.from_numpy(ref.unpack_rows(cache.cpu().numpy(), d)).cuda()
+    q = _queries(pg.rows, d, 243)
+    idx = torch.from_numpy(ref.random_selection(pg, 64, 244)).cuda()
+    out, lse, status = _attend(dsa, pb, True, q, cache, idx, pg.rows)
+    assert status == 0
+    ref.check_attention_rows(out, lse, q, values, idx, pg, d["d_qk"] ** -0.5, d,
+                             rows=range(0, pg.rows, 7))
+
+
+@pytest.mark.parametrize("q8", [True, False], ids=["q8", "bf16"])
 def test_attention_ignores_unselected_nan(dsa, q8):
     """NaN and infinities in cache rows that no entry selects (and in unused pages) change
     nothing."""
