@@ -425,7 +425,9 @@ __global__ void __launch_bounds__(512, 1)
   if (warp < 8) cluster_wait();
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
-  const int n = warp < 8 && abort_s ? 0 : n_act;
+  // (one answer for a warp's lanes, whenever another warp gives up)
+  auto aborted = [&] { return __any_sync(0xffffffffu, abort_s) != 0; };
+  const int n = warp < 8 && aborted() ? 0 : n_act;
   auto mask_of = [&](int i) -> uint64_t {
     if (dense) return i == n - 1 ? sMask[0] : ~0ull;
     return sMask[sTiles[i]];
@@ -596,7 +598,7 @@ __global__ void __launch_bounds__(512, 1)
       if (i == C::PRE_TILES) {                   // from here on the slots were Q's staging area
         cluster_wait();
         joined = true;
-        if (abort_s) return false;
+        if (aborted()) return false;
       }
       const uint8_t* const src[2] = {row_ptr(rows, rsub), row_ptr(rows, rsub + 4)};
       if ((i & 1) == c) {                        // the rotary block, on this CTA's tiles
@@ -700,7 +702,7 @@ __global__ void __launch_bounds__(512, 1)
     const bool counts = (q & 1) == 0;           // one of the tile's two warps expects the bytes
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     float m_mine = -INFINITY, l_sum = 0.f;      // l_sum: this warp's tiles, to reference m_mine
-    bool ok = !abort_s;
+    bool ok = !aborted();
 #pragma unroll 1
     for (int i = t; i < n && ok; i += 2) {
       const uint32_t ph = (i >> 1) & 1;
