@@ -175,7 +175,6 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
   uint32_t* sHist = reinterpret_cast<uint32_t*>(done + 1);   // [QPG][kIdxHistBins]
   const bool hist_on = C::HIST && p.hist != nullptr;
   __shared__ uint32_t tmem_base_s;
-  __shared__ int abort_s;
   __shared__ int last_s[2];   // the last tile each producer issued (-1: none)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -237,7 +236,6 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
     }
     mbar_init(smem_u32(qbar), 1);
     mbar_init(smem_u32(done), 1);
-    abort_s = 0;
     fence_mbar_init();
   }
   if (hist_on)
@@ -279,7 +277,6 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
         const int s = it % C::STAGES;
         if (it >= C::STAGES &&
             !thread_wait(smem_u32(&empty[s]), ((it / C::STAGES) - 1) & 1)) {
-          abort_s = 1;
           if (p.status) atomicOr(p.status, kStatusTimeout);
           break;
         }
@@ -436,10 +433,7 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
       }
       __syncwarp();
     }
-    if (!ok) {
-      abort_s = 1;
-      if (lane == 0 && p.status) atomicOr(p.status, kStatusTimeout);
-    }
+    if (!ok && lane == 0 && p.status) atomicOr(p.status, kStatusTimeout);
     __syncwarp();
     if (elect_one()) umma_commit(smem_u32(done));
     __syncwarp();
@@ -473,8 +467,7 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
       return true;
     };
     auto give_up = [&] {
-      abort_s = 1;
-      if (p.status) atomicOr(p.status, kStatusTimeout);
+      if (lane == 0 && p.status) atomicOr(p.status, kStatusTimeout);
     };
     if constexpr (C::REG_C) {
       float2 c_row[H_I / 2];
