@@ -100,11 +100,17 @@ __device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, uint32_t src, ui
           "r"(dst), "r"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
-// Arrive on a barrier of another CTA of the cluster without releasing anything: it says that
-// values have been read (and are in registers), not that something was written.  The releasing
-// form waits for this thread's stores to reach the other SM first, 500 cycles and more.
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrive on a barrier of another CTA of the cluster when what this thread (and, behind a
+// __syncwarp, its warp) read from its own CTA's shared memory has been read: the other CTA may
+// overwrite it once its wait has passed.  The fence releases the accesses to this CTA's shared
+// memory alone.  An arrival with release semantics of its own also waits for everything the thread
+// stored elsewhere: 2048 rows over 8-bit rows 1850 us instead of 1449, 1000 rows over bf16 835
+// instead of 680.
+__device__ __forceinline__ void mbar_arrive_cluster_read(uint32_t bar) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+      : "memory");
 }
 // Arrive once on the barrier at this offset in every CTA of `mask` when every tcgen05 operation
 // this thread issued so far has completed.
@@ -750,11 +756,8 @@ __global__ void __launch_bounds__(512, 1)
           s[2 * g] = __fadd2_rn(s[2 * g], make_float2(x.x, x.y));
           s[2 * g + 1] = __fadd2_rn(s[2 * g + 1], make_float2(x.z, x.w));
         }
-        // (the sums pin the loads before the arrival)
-#pragma unroll
-        for (int e = 16 * h; e < 16 * h + 16; ++e) asm volatile("" : "+f"(s[e].x), "+f"(s[e].y));
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(x_free_peer + h * 8);
+        __syncwarp();                               // every lane has read its logits
+        if (lane == 0) mbar_arrive_cluster_read(x_free_peer + h * 8);
       }
       if (!ok) break;
       if (mask_of(i) != ~0ull) {                  // invalid keys: -inf, so p = 0
