@@ -215,9 +215,12 @@ __global__ void __launch_bounds__(512, 1)
   float* sRef = sAlpha + 2 * 64;                  // [2][64 heads] the reference after a tile
   float* sSum = sRef + 2 * 64;                    // [2 warps][sum, reference][64 heads]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sSum + 4 * 64);
-  // after the last tile, over the rows that no one reads any more (sSum is not: with one tile a
-  // softmax warp has none and writes its sums at once)
-  float* sInv = reinterpret_cast<float*>(sPhys);  // [128] 1 / sum
+  // [128] 1 / sum, half of it written by the partner after its last tile.  Nothing before the tiles
+  // touches this memory, and the factors in it have been read in front of the last PV, which the
+  // partner's softmax warps wait for.  (Over the key rows, a CTA without a tile could still be
+  // storing them when its partner writes; sSum too: with one tile a softmax warp has none and
+  // writes its sums at once.)
+  float* sInv = sAlpha;
   uint64_t* v_full = bars;           // [V_SLOTS] every gathering thread
   uint64_t* v_empty = bars + 5;      // [V_SLOTS] PV commit
   uint64_t* r_full = bars + 10;      // every gathering thread (rotary copies landed)
@@ -945,7 +948,8 @@ __global__ void __launch_bounds__(D_V / 4) dsa_paged_combine_kernel(const PagedM
 #pragma unroll
   for (int s = 0; s < MAX_SPLITS; ++s) {
     if (s >= p.splits) break;
-    const float w = lse[s] == -INFINITY ? 0.f : expf(lse[s] - m);   // a NaN LSE stays NaN
+    if (lse[s] == -INFINITY) continue;            // a split without keys
+    const float w = expf(lse[s] - m);             // (a NaN LSE stays NaN)
     wsum += w;
     acc.x = fmaf(w, v[s].x, acc.x);
     acc.y = fmaf(w, v[s].y, acc.y);
