@@ -487,11 +487,12 @@ DSA_API dsa_status_t dsa_read_device_status(const int32_t* dev_status, dsa_strea
                                     int32_t* raw);
 
 /* Diagnostics: checks that a wait which never completes ends instead of hanging.  Launches one
- * CTA of two warps that wait, with the same bounded wait every kernel above uses (2 s limit), on
- * an mbarrier nothing arrives at; each warp that gives up ORs DSA_DEVICE_TIMEOUT into
- * *dev_status (device, 4-byte aligned, caller-owned) and the CTA then exits normally, leaving the
- * context usable.  Asynchronous on `stream`, which stays busy for about 2 s; read the word with
- * dsa_read_device_status, which then returns DSA_ERR_TIMEOUT. */
+ * CTA whose warps wait on an mbarrier nothing arrives at, each with another of the bounded waits
+ * that the kernels above use (limits of 2 s by the clock, or of as many sleeping polls as take 2.1 s);
+ * when every one has given up, DSA_DEVICE_TIMEOUT is ORed into *dev_status (device, 4-byte aligned,
+ * caller-owned).  The CTA exits normally, leaving the context usable.  Asynchronous on `stream`,
+ * which stays busy for about 2 s; read the word with dsa_read_device_status, which then returns
+ * DSA_ERR_TIMEOUT. */
 DSA_API dsa_status_t dsa_selftest_wait_timeout(int32_t* dev_status, dsa_stream_t stream);
 
 /* Diagnostics: the rate of distributed-shared-memory traffic between the two CTAs of a cluster,

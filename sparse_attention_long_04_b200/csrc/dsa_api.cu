@@ -1098,23 +1098,37 @@ dsa_status_t kl_backward_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const ui
 
 // ---------------------------------------------------------------- bounded-wait self-test
 
-// One CTA waits on an mbarrier that nothing arrives at, with the wait every kernel here uses
-// (lane 0 polls, 2 s limit, then the whole warp gives up).  As in the kernels above, the first
-// warp to give up raises the CTA's abort flag so that the other ends its wait early; each warp
-// records a timeout in the status word and the CTA then exits normally.
-__global__ void __launch_bounds__(64) dsa_selftest_wait_kernel(int32_t* status) {
+// One CTA whose warps wait on an mbarrier that nothing arrives at, each with another of the bounded
+// waits that the kernels here use, at the limits they use: warps 0 and 1 warp_mbar_wait (lane 0
+// polls, 2 s by the clock; the first to give up raises the abort flag that ends the other's wait
+// early), warps 2 and 3 warp_wait within the CTA and with cluster acquire, warp 4 one thread's
+// thread_wait (kPolls sleeping polls, 2.1 s).  The timeout is recorded when every one has given up; the
+// CTA then exits normally.
+constexpr int kSelftestWarps = 5;
+__global__ void __launch_bounds__(32 * kSelftestWarps) dsa_selftest_wait_kernel(int32_t* status) {
   __shared__ __align__(8) uint64_t bar;
   __shared__ volatile int abort_flag;
+  __shared__ int gave_up;
+  const int warp = threadIdx.x / 32;
+  const bool first = (threadIdx.x & 31) == 0;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bar), 1);
     abort_flag = 0;
+    gave_up = 0;
     fence_mbar_init();
   }
   __syncthreads();
-  if (!warp_mbar_wait(smem_u32(&bar), 0, &abort_flag) && (threadIdx.x & 31) == 0) {
-    abort_flag = 1;
-    atomicOr(status, kStatusTimeout);
+  bool passed = false;
+  if (warp < 2) passed = warp_mbar_wait(smem_u32(&bar), 0, &abort_flag);
+  else if (warp == 2) passed = warp_wait(smem_u32(&bar), 0);
+  else if (warp == 3) passed = warp_wait<true>(smem_u32(&bar), 0);
+  else if (first) passed = thread_wait(smem_u32(&bar), 0);
+  if (!passed && first) {
+    if (warp < 2) abort_flag = 1;
+    atomicAdd(&gave_up, 1);
   }
+  __syncthreads();
+  if (threadIdx.x == 0 && gave_up == kSelftestWarps) atomicOr(status, kStatusTimeout);
 }
 
 // ------------------------------------------------------- distributed shared memory probe
@@ -1652,7 +1666,7 @@ dsa_status_t dsa_selftest_wait_timeout(int32_t* dev_status, dsa_stream_t stream)
   if (dev_status == nullptr) return DSA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(dev_status) & 3u) != 0)
     return DSA_ERR_MISALIGNED;
-  dsa_selftest_wait_kernel<<<1, 64, 0, reinterpret_cast<cudaStream_t>(stream)>>>(dev_status);
+  dsa_selftest_wait_kernel<<<1, 32 * kSelftestWarps, 0, reinterpret_cast<cudaStream_t>(stream)>>>(dev_status);
   return launch_status();
 }
 

@@ -125,7 +125,7 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-constexpr uint32_t kPollNs = 1000, kPolls = 1u << 22;   // see warp_wait
+constexpr uint32_t kPollNs = 1000, kPolls = 1u << 19;   // see warp_wait
 
 // One poll of `bar` by every lane; kHint: the lanes may sleep until the phase completes (or
 // kPollNs).  kCluster: acquires what the other CTA of the cluster wrote before it arrived.
@@ -161,11 +161,11 @@ __device__ __forceinline__ uint32_t poll_bar(uint32_t bar, uint32_t parity) {
 
 // Whole-warp wait for phase `parity` of `bar`; all lanes return the same result, false when the
 // wait gave up.  The first poll has no suspend-time hint, which a completed phase answers in 14
-// cycles (46 with the hint, 195 for a poll by lane 0 and a shuffle); the polls after it sleep up
-// to kPollNs, so that waiting warps leave the pipes to the others, and are kPolls at most: at
-// least 40 ms of 20-cycle polls, at most some 4 s of full sleeps.  The limit is a count, not a
-// clock, to keep the many inlined copies short: the kernel's loops compete for the instruction
-// caches.
+// cycles (46 with the hint, 195 for a poll by lane 0 and a shuffle); the polls after it sleep until
+// the phase completes, 4 us at most (measured, with the hint of kPollNs), so that waiting warps leave
+// the pipes to the others.  kPolls of them make the limit 2.1 s, the one of mbar_wait.  It is a count,
+// not a clock, to keep the many inlined copies short: the kernel's loops compete for the
+// instruction caches.
 template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok = poll_bar<kCluster, false>(bar, parity);
