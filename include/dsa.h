@@ -154,7 +154,8 @@ DSA_API dsa_status_t dsa_indexer_scores(const dsa_dims_t* dims, const dsa_seqs_t
 /* Stage 2.  Exact top-k of each row of `scores` (layout as written by dsa_indexer_scores)
  * over keys 0..pos(t).  idx int32 [row_count, topk]: the selected LOGICAL key indices in
  * increasing order, then -1 padding when pos(t) + 1 < topk.  The set is unique: larger
- * score first, equal scores broken by the smaller index (-0 and +0 compare equal).
+ * score first, equal scores broken by the smaller index (-0 and +0 compare equal, a NaN
+ * compares equal to +infinity).
  *   hist  optional: the histograms dsa_indexer_scores counted while writing these same rows
  *         of `scores` (exact counts of each row's keys 0..pos(t); anything else gives a wrong
  *         selection).  The selection then starts from them and reads each score once; on

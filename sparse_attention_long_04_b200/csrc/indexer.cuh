@@ -67,9 +67,10 @@ struct IndexerParams {
 
 constexpr int kIdxHistBins = 2048;   // top 11 bits of the order-preserving score key
 
-// Order-preserving 32-bit key of a score (unsigned order = float order, -0 folded onto +0).
+// Order-preserving 32-bit key of a score (unsigned order = float order, -0 folded onto +0, a NaN
+// taken as +infinity).
 __device__ __forceinline__ uint32_t order_key(float f) {
-  uint32_t u = __float_as_uint(f);
+  uint32_t u = __float_as_uint(fminf(f, INFINITY));
   if ((u << 1) == 0) u = 0;
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }

@@ -68,8 +68,12 @@ __host__ __device__ constexpr int topk_smem_bytes(int slice) {
   return kTopkFixedSmem + 2 * ((slice + 31) / 32) * 4;
 }
 
+// What the selection compares: the score, a NaN taken as +infinity (a float comparison is false for
+// a NaN either way, so that it would count in its bin and never be taken).
+__device__ __forceinline__ float ranked(float f) { return fminf(f, INFINITY); }
+
 __device__ __forceinline__ uint32_t score_key(float f) {
-  uint32_t u = __float_as_uint(f);
+  uint32_t u = __float_as_uint(ranked(f));
   if ((u << 1) == 0) u = 0;                       // -0 == +0
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kTopkThreads, 2) dsa_topk_kernel(const TopkPar
     for (int u = 0; u < U; ++u) {
       const int rd = rd0 + u * kTopkWarps;
       if (rd >= nrounds) break;
-      const float ve[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      const float ve[4] = {ranked(v[u].x), ranked(v[u].y), ranked(v[u].z), ranked(v[u].w)};
       uint32_t cw[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
