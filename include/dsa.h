@@ -311,7 +311,9 @@ DSA_API dsa_status_t dsa_forward_rows(const dsa_dims_t* dims, const dsa_seqs_t* 
  * p % block_size, or b * max_seqlen + p when block_table is NULL:
  *   k_new     fp32 [batch, d_idx]: the new token's indexer key, quantised per token: scale =
  *             amax / 448 in fp32 (1 when amax = 0), codes = the e4m3 value nearest to x / scale
- *             (ties to even, saturating at +-448)
+ *             (the quotient in fp32; ties to even, saturating at +-448).  A key that holds an
+ *             infinity or a NaN gets a NaN scale and zero codes; its scores are NaN, which the
+ *             selection ranks with +infinity
  *   kv_new    bf16 [batch, d_qk]: the new token's latent row, copied unchanged
  *   k_cache   e4m3 [num_kv_rows, d_idx], k_scale_cache fp32 [num_kv_rows], kv_cache bf16
  *             [num_kv_rows, d_qk]: caller-owned caches, written at the one row per sequence

@@ -367,13 +367,22 @@ static uint8_t e4m3_round(float yf) {
 
 /* Quantise n_rows rows of d fp32 values, each with its own scale: amax = max |x| over the
  * row, scale = amax / 448 in fp32 (1 when amax = 0), y = x / scale in fp32, clamped to
- * [-448, 448], then rounded to the nearest E4M3 value (ties to even).  codes [n_rows, d],
- * scales [n_rows]. */
+ * [-448, 448], then rounded to the nearest E4M3 value (ties to even).  A row that holds an
+ * infinity or a NaN gets a NaN scale and zero codes.  codes [n_rows, d], scales [n_rows]. */
 void dsa_oracle_quantize_e4m3(int n_rows, int d, const float* x, uint8_t* codes, float* scales) {
   for (int r = 0; r < n_rows; ++r) {
     const float* xr = x + (int64_t)r * d;
     float amax = 0.0f;
-    for (int i = 0; i < d; ++i) amax = fmaxf(amax, fabsf(xr[i]));
+    int finite = 1;
+    for (int i = 0; i < d; ++i) {
+      finite &= isfinite(xr[i]) != 0;
+      amax = fmaxf(amax, fabsf(xr[i]));
+    }
+    if (!finite) {
+      scales[r] = NAN;
+      memset(codes + (int64_t)r * d, 0, (size_t)d);
+      continue;
+    }
     const float scale = amax > 0.0f ? amax / 448.0f : 1.0f;
     scales[r] = scale;
     for (int i = 0; i < d; ++i) {

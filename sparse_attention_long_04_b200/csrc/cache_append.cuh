@@ -1,10 +1,11 @@
 // Decode cache append: the step upstream of the indexer.  Each decode sequence b has one new
 // token at position p = seq_lens[b] - 1.  Its indexer key k_new[b] (fp32, D_I values) is
 // quantised with one scale per token (scale = amax / 448 in fp32, 1 when amax = 0; codes =
-// the e4m3 value nearest to x / scale, ties to even, saturating at +-448) and written with its
-// scale, and its latent row kv_new[b] (bf16, D_QK values) is copied, at the physical row
-// block_table[b][p / bs] * bs + p % bs (row b * max_seqlen + p without a block table).  The
-// caches it fills are the indexer's "FP8 index" keys and the latent rows the sparse attention
+// the e4m3 value nearest to x / scale, ties to even, saturating at +-448; a NaN scale and zero
+// codes for a key with an infinity or a NaN) and written with its scale, and its latent row
+// kv_new[b] (bf16, D_QK values) is copied, at the physical row block_table[b][p / bs] * bs + p % bs
+// (row b * max_seqlen + p without a block table).  The caches it fills are the indexer's "FP8
+// index" keys and the latent rows the sparse attention
 // gathers ("FP8 index -> top-k selection -> sparse core attention", "DeepSeek V3.2-Exp Cuts
 // Long-Context Costs with DeepSeek Sparse Attention (DSA)", pipeline summary).
 //
@@ -13,9 +14,7 @@
 // position or block falls outside the caches is skipped and reported.  The key cache may hold
 // each 64-row block's scales right after its key rows (paged decode, no separate scale array).
 #pragma once
-#include <cuda_fp8.h>
-
-#include "sm100.cuh"
+#include "q8_row.cuh"
 
 namespace dsa {
 
@@ -67,19 +66,8 @@ __global__ void __launch_bounds__(128) dsa_cache_append_kernel(const AppendParam
 #pragma unroll
     for (int i = 0; i < PER; ++i) x[i] = src[i];
   }
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) amax = fmaxf(amax, fabsf(x[i]));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float scale = amax > 0.f ? amax / 448.f : 1.f;
-  uint32_t packed = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const float y = fminf(fmaxf(x[i] / scale, -448.f), 448.f);
-    const uint32_t c = __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
-    packed |= c << (8 * i);
-  }
+  uint32_t packed;
+  const float scale = q8_key(x, &packed);
   // the key row and its scale: separate arrays, or inside the row's 64-row block
   const int64_t blk = row / 64, r64 = row % 64;
   uint8_t* krow = p.k_scale != nullptr ? p.k_cache + row * D_I

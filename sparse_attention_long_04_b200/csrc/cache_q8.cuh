@@ -21,8 +21,8 @@ struct CacheWriteParams {
   int32_t* status;
 };
 
-// One warp per new token.  The indexer key: one fp32 scale a token, amax / 448, as the decode
-// append computes it.  The latent row: lane l holds values 16 l .. 16 l + 15, so the 8 lanes of
+// One warp per new token.  The indexer key: one fp32 scale a token (q8_key, as in the decode
+// append).  The latent row: lane l holds values 16 l .. 16 l + 15, so the 8 lanes of
 // a 128-value group reduce its largest magnitude in three shuffles and every lane stores one
 // 16-byte chunk of codes.
 template <int D_I, int D_QK, int D_V, bool kQ8>
@@ -68,15 +68,8 @@ __global__ void __launch_bounds__(128) dsa_cache_write_kernel(const CacheWritePa
     return;
   }
   // ---- indexer key
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) amax = fmaxf(amax, fabsf(x[i]));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float scale = amax > 0.f ? amax / 448.f : 1.f;
-  uint32_t packed = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) packed |= q8_code(x[i] / scale) << (8 * i);
+  uint32_t packed;
+  const float scale = q8_key(x, &packed);
   const int64_t blk = dst / 64, r64 = dst % 64;
   const bool apart = p.k_scale != nullptr;     // scales in their own array
   uint8_t* page = p.k_cache + blk * (64 * (D_I + 4));

@@ -1,5 +1,5 @@
 // A row of the 8-bit latent cache and its arithmetic, shared by the kernels that write, read and
-// attend over it.
+// attend over it, and the 8-bit form of an indexer key.
 //
 // Layout of one row (D_QK latent dims, the first D_V of them values):
 //   bytes [0, D_V)                     e4m3 codes of the D_V latent values
@@ -53,6 +53,26 @@ __device__ __forceinline__ int q8_exponent(uint32_t amax) {
 // The e4m3 code nearest to y (ties to even, saturating at +-448; y is finite).
 __device__ __forceinline__ uint32_t q8_code(float y) {
   return __nv_cvt_float_to_fp8(fminf(fmaxf(y, -448.f), 448.f), __NV_SATFINITE, __NV_E4M3);
+}
+
+// A token's indexer key, PER consecutive values a lane of a converged warp: returns its scale, amax /
+// 448 in fp32 (1 for a key of zeros), and the lane's codes of x / scale (rounded to fp32 first, so
+// that a code can be one step off the exact quotient's at a tie).  As in a latent group, a key that
+// holds an infinity or a NaN gets a NaN scale and zero codes: its scores are NaN, not those of
+// another key.
+template <int PER>
+__device__ __forceinline__ float q8_key(const float (&x)[PER], uint32_t* codes) {
+  uint32_t top = 0;                                // largest magnitude (NaN above infinity)
+#pragma unroll
+  for (int i = 0; i < PER; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  top = __reduce_max_sync(0xffffffffu, top);
+  const float amax = __uint_as_float(top);
+  *codes = 0;
+  if (top >= 0x7F800000u) return __uint_as_float(0x7FFFFFFFu);
+  const float scale = amax > 0.f ? amax / 448.f : 1.f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) *codes |= q8_code(x[i] / scale) << (8 * i);
+  return scale;
 }
 
 // Two e4m3 codes (the low bytes of the halves of z) times a power of two, as two bf16.  A code's
