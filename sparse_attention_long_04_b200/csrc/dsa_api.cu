@@ -231,6 +231,13 @@ bool dense_ok(const dsa_dims_t& d, const dsa_seqs_t* s, int32_t row_begin, int32
   return s->mode != DSA_DECODE || max_keys(s, row_begin, row_count) <= d.topk;
 }
 
+// The paged attention resolves the pages of a row's keys up front: kMaxDenseTiles of them (131072
+// keys) without indices.  The limit is one of the context and does not move with the split count,
+// which depends on the rows and the device.
+bool paged_dense_ok(const dsa_seqs_t* s, const int32_t* idx) {
+  return idx != nullptr || ceil_div(s->max_seqlen, 64) <= kMaxDenseTiles;
+}
+
 // The training target without indices writes topk entries per row: rows of at most topk keys.
 bool dense_target_ok(const dsa_dims_t& d, const dsa_seqs_t* s, int32_t row_begin,
                      int32_t row_count) {
@@ -687,9 +694,6 @@ dsa_status_t paged_mla_impl(const dsa_dims_t& d, const dsa_seqs_t& s, const uint
   prm.splits = splits;
   prm.scale_log2 = d.softmax_scale * 1.4426950408889634f;
   prm.status = status;
-  // without indices a split's pages are resolved up front
-  if (idx == nullptr && ceil_div(ceil_div(s.max_seqlen, 64), splits) > kMaxDenseTiles)
-    return DSA_ERR_UNSUPPORTED_SHAPE;
   if (splits > 1) {
     if (ws == nullptr || ws_bytes < mla_ws_bytes(d, splits, row_count))
       return DSA_ERR_WORKSPACE_TOO_SMALL;
@@ -1359,6 +1363,7 @@ dsa_status_t dsa_sparse_mla_fwd(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
   if ((e = check_rows(seqs, row_begin, row_count)) != DSA_OK) return e;
   if (!q || !kv || !out || !lse) return DSA_ERR_INVALID_ARG;
   if (idx == nullptr && !dense_ok(*dims, seqs, row_begin, row_count)) return DSA_ERR_INVALID_ARG;
+  if (seqs->mode == DSA_CHUNK && !paged_dense_ok(seqs, idx)) return DSA_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(q) || !aligned16(kv) || !aligned16(idx) || !aligned16(out) || !aligned16(lse) ||
       !aligned16(workspace))
     return DSA_ERR_MISALIGNED;
@@ -1560,6 +1565,7 @@ dsa_status_t dsa_sparse_mla_fwd_q8(const dsa_dims_t* dims, const dsa_seqs_t* seq
   if (!mla_shape_ok(*dims)) return DSA_ERR_UNSUPPORTED_SHAPE;
   if ((e = check_rows(seqs, row_begin, row_count)) != DSA_OK) return e;
   if (!q || !kv8 || !out || !lse) return DSA_ERR_INVALID_ARG;
+  if (!paged_dense_ok(seqs, idx)) return DSA_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(q) || !aligned16(kv8) || !aligned16(idx) || !aligned16(out) || !aligned16(lse) ||
       !aligned16(workspace))
     return DSA_ERR_MISALIGNED;
@@ -1779,6 +1785,7 @@ dsa_status_t dsa_sparse_mla_fwd_noalloc(const dsa_dims_t* dims, const dsa_seqs_t
   if ((e = check_rows(seqs, row_begin, row_count)) != DSA_OK) return e;
   if (!q || !kv || !out || !lse) return DSA_ERR_INVALID_ARG;
   if (idx == nullptr && !dense_ok(*dims, seqs, row_begin, row_count)) return DSA_ERR_INVALID_ARG;
+  if (seqs->mode == DSA_CHUNK && !paged_dense_ok(seqs, idx)) return DSA_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(q) || !aligned16(kv) || !aligned16(idx) || !aligned16(out) || !aligned16(lse))
     return DSA_ERR_MISALIGNED;
   DeviceInfo info;
