@@ -42,7 +42,8 @@
  *   - `dev_status` is an optional caller-owned DEVICE int32.  Kernels OR in
  *     DSA_DEVICE_TIMEOUT when a bounded wait gave up (the kernel then unwinds instead of
  *     hanging) and DSA_DEVICE_BAD_INDEX when an index or block-table entry points outside
- *     the caches (that entry is then skipped).  Clear it before the call; read it with
+ *     the caches (that entry is then skipped; the keys of a page that lies outside, or of
+ *     which the caches hold only a part, score 0).  Clear it before the call; read it with
  *     dsa_read_device_status.  NULL disables the reporting (the kernels still unwind).
  *   - Alignment: every tensor pointer must be 16-byte aligned, ld_scores a multiple of 4;
  *     otherwise DSA_ERR_MISALIGNED.

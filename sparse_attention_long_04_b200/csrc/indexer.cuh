@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
                           ? static_cast<uint32_t>((avail < 68 ? avail : int64_t(68)) / 4 * 16)
                           : 0u;
             const int lead = static_cast<int>(y[hlf] - a0[hlf]);
-            sRow0[s * 2 + hlf] = y[hlf];
+            sRow0[s * 2 + hlf] = ok[hlf] ? y[hlf] : -64;     // (no page: no scales, scores of 0)
             sFirst[s * 2 + hlf] = hlf * 80 + lead;
             sValid[s * 2 + hlf] = static_cast<int32_t>(sb[hlf] / 4) - lead;
           }
@@ -490,10 +490,12 @@ __global__ void __launch_bounds__(IndexerCfg<H_I, D_I, QPG, kChunk>::THREADS, QP
         if (it >= n_tiles || blk >= n_halves) return -1;
         return table != nullptr ? __ldg(table + blk) : blk;
       };
+      // (a page is inside the caches when all of it is: the keys of others were not loaded)
+      const int64_t row_end = table != nullptr ? p.num_kv_rows / 64 * 64 : p.num_kv_rows;
       auto scale_of = [&](int32_t blk) -> float {
         const int j = (quad & 1) * 32 + lane;
         const int64_t row = (table != nullptr ? 0 : first) + static_cast<int64_t>(blk) * 64 + j;
-        if (blk < 0 || row >= p.num_kv_rows) return 0.f;
+        if (blk < 0 || row >= row_end) return 0.f;   // (outside the caches: a score of 0)
         return p.k_scale != nullptr
                    ? __ldg(p.k_scale + row)
                    : __ldg(reinterpret_cast<const float*>(
