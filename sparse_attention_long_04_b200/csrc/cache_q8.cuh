@@ -61,9 +61,10 @@ __global__ void __launch_bounds__(128) dsa_cache_write_kernel(const CacheWritePa
   int b, pos;
   bool bad;
   paged_row(p.s, row, &b, &pos, &bad);
-  // a context above max_seqlen would move the token: it is skipped, as one without a place is
+  // a context above max_seqlen would move the token: it is skipped, as one without a place is, and one
+  // whose page the caches hold only in part (the indexer would not read it)
   const int64_t dst = bad || pos < 0 ? -1 : paged_phys(p.s, b, pos);
-  if (dst < 0) {
+  if (dst < 0 || (p.s.block_table != nullptr && (dst / 64 + 1) * 64 > p.s.num_kv_rows)) {
     if (lane == 0 && p.status) atomicOr(p.status, kStatusBadIndex);
     return;
   }

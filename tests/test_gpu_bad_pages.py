@@ -1,5 +1,5 @@
 """Pages outside the caches, whole or in part: their keys score 0, the other keys as without the bad
-page."""
+page, and no new token is written there."""
 import numpy as np
 import pytest
 import torch
@@ -56,3 +56,31 @@ def test_scores_of_a_bad_page_are_zero(dsa, d, mode, layout):
             for j, _ in bad[b]:
                 want[j * 64:min((j + 1) * 64, pos + 1)] = 0
             assert torch.equal(slab[r], want), r
+
+
+@pytest.mark.parametrize("q8", [True, False], ids=["q8", "bf16"])
+@pytest.mark.parametrize("mode", ["decode", "chunk"])
+def test_append_into_a_page_in_part_outside(dsa, q8, mode):
+    """A page of which the caches hold only the first rows takes no token in either mode (the indexer
+    would not read it)."""
+    d = FULL
+    new, ctx = ([1, 1], [100, 70]) if mode == "decode" else ([2, 3], [100, 70])
+    pg = Pages(new, ctx, seed=83, spare=0)
+    pg.table[:, :2] = [[0, 3], [1, 2]]              # the last page under sequence 0's new tokens
+    pg.d_table.copy_(torch.from_numpy(pg.table))
+    rows = pg.kv_rows
+    pg.kv_rows -= 4                                 # the last page holds 60 rows
+    pb = pg.problem(dsa, d, 64, mode)
+    rb = ref.row_bytes(d) if q8 else 2 * d["d_qk"]
+    kv = torch.full((rows, rb), 7, dtype=torch.uint8, device="cuda")
+    k8 = torch.full((rows, d["d_idx"]), 7, dtype=torch.uint8, device="cuda")
+    ks = torch.full((rows,), 7.0, device="cuda")
+    k_new = torch.randn(pg.rows, d["d_idx"], device="cuda")
+    kv_new = ref.latents(pg.rows, d, 84)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call = dsa.dsa_cache_append_q8 if q8 else dsa.dsa_cache_append
+    assert call(pb, k_new, kv_new, k8, ks, kv, status) == dsa.DSA_OK
+    assert int(status.item()) == dsa.DSA_DEVICE_BAD_INDEX
+    want = {int(x) for x in pg.phys(1, np.arange(ctx[1] - new[1], ctx[1]))}
+    assert set(np.nonzero(to_np(ks) != 7.0)[0].tolist()) == want
+    assert set(np.nonzero((to_np(kv) != 7).any(axis=1))[0].tolist()) <= want
