@@ -115,7 +115,8 @@ typedef struct {
   int32_t d_v;          /* value dims = the first d_v dims of a latent KV row */
   int32_t topk;         /* keys kept per query row */
   int32_t block_size;   /* page size of the decode caches (64) */
-  float softmax_scale;  /* sigma in the logits sigma * q.kv */
+  float softmax_scale;  /* sigma in the logits sigma * q.kv, positive (checked for attention over
+                           chunks and over the 8-bit cache: DSA_ERR_INVALID_ARG) */
 } dsa_dims_t;
 
 typedef struct {

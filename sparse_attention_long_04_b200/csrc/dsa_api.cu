@@ -238,6 +238,12 @@ bool paged_dense_ok(const dsa_seqs_t* s, const int32_t* idx) {
   return idx != nullptr || ceil_div(s->max_seqlen, 64) <= kMaxDenseTiles;
 }
 
+// The paged attention masks keys by logits of -inf and takes maxima before the scale, which both need
+// a positive one.
+bool paged_scale_ok(const dsa_dims_t& d) {
+  return d.softmax_scale > 0.f && std::isfinite(d.softmax_scale);
+}
+
 // The training target without indices writes topk entries per row: rows of at most topk keys.
 bool dense_target_ok(const dsa_dims_t& d, const dsa_seqs_t* s, int32_t row_begin,
                      int32_t row_count) {
@@ -890,6 +896,7 @@ dsa_status_t forward_window(const dsa_dims_t& d, const dsa_seqs_t& s, int64_t w0
   if (!q_idx || !q_scale || !w || !k_idx || !q || !kv_rows || !out || !lse)
     return DSA_ERR_INVALID_ARG;
   if (sel_out != nullptr && idx_out == nullptr) return DSA_ERR_INVALID_ARG;
+  if ((s.mode == DSA_CHUNK || q8) && !paged_scale_ok(d)) return DSA_ERR_INVALID_ARG;
   if (k_scale == nullptr && !interleaved_ok(s)) return DSA_ERR_INVALID_ARG;
   if (!aligned16(q_idx) || !aligned16(k_idx) || !aligned16(k_scale) || !aligned16(q) ||
       !aligned16(kv_rows) || !aligned16(out) || !aligned16(lse) || !aligned16(idx_out) ||
@@ -1363,6 +1370,7 @@ dsa_status_t dsa_sparse_mla_fwd(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
   if ((e = check_rows(seqs, row_begin, row_count)) != DSA_OK) return e;
   if (!q || !kv || !out || !lse) return DSA_ERR_INVALID_ARG;
   if (idx == nullptr && !dense_ok(*dims, seqs, row_begin, row_count)) return DSA_ERR_INVALID_ARG;
+  if (seqs->mode == DSA_CHUNK && !paged_scale_ok(*dims)) return DSA_ERR_INVALID_ARG;
   if (seqs->mode == DSA_CHUNK && !paged_dense_ok(seqs, idx)) return DSA_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(q) || !aligned16(kv) || !aligned16(idx) || !aligned16(out) || !aligned16(lse) ||
       !aligned16(workspace))
@@ -1565,6 +1573,7 @@ dsa_status_t dsa_sparse_mla_fwd_q8(const dsa_dims_t* dims, const dsa_seqs_t* seq
   if (!mla_shape_ok(*dims)) return DSA_ERR_UNSUPPORTED_SHAPE;
   if ((e = check_rows(seqs, row_begin, row_count)) != DSA_OK) return e;
   if (!q || !kv8 || !out || !lse) return DSA_ERR_INVALID_ARG;
+  if (!paged_scale_ok(*dims)) return DSA_ERR_INVALID_ARG;
   if (!paged_dense_ok(seqs, idx)) return DSA_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(q) || !aligned16(kv8) || !aligned16(idx) || !aligned16(out) || !aligned16(lse) ||
       !aligned16(workspace))
@@ -1785,6 +1794,7 @@ dsa_status_t dsa_sparse_mla_fwd_noalloc(const dsa_dims_t* dims, const dsa_seqs_t
   if ((e = check_rows(seqs, row_begin, row_count)) != DSA_OK) return e;
   if (!q || !kv || !out || !lse) return DSA_ERR_INVALID_ARG;
   if (idx == nullptr && !dense_ok(*dims, seqs, row_begin, row_count)) return DSA_ERR_INVALID_ARG;
+  if (seqs->mode == DSA_CHUNK && !paged_scale_ok(*dims)) return DSA_ERR_INVALID_ARG;
   if (seqs->mode == DSA_CHUNK && !paged_dense_ok(seqs, idx)) return DSA_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(q) || !aligned16(kv) || !aligned16(idx) || !aligned16(out) || !aligned16(lse))
     return DSA_ERR_MISALIGNED;
