@@ -124,3 +124,43 @@ def test_short_contexts_of_a_long_batch_repeat_exactly(dsa, q8):  # noqa: F811
             ref.check_attention_rows(out, lse, q, values, idx, pg, d["d_qk"] ** -0.5, d)
         for a, b in zip(first, (idx, out, lse)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("mode,q8", [("decode", True), ("chunk", True), ("chunk", False)])
+@pytest.mark.parametrize("every", [True, False], ids=["every", "selected"])
+def test_attention_sees_the_token_written_just_before(dsa, mode, q8, every):  # noqa: F811
+    """Append and attention back to back, the same places overwritten step after step: each step
+    reads the rows of its own append, as with the device idle in between."""
+    d = FULL
+    batch = 40
+    new = [1] * batch if mode == "decode" else [1, 3] * (batch // 2)
+    pg = Pages(new, [200 + 7 * b for b in range(batch)], seed=45)
+    pb = pg.problem(dsa, d, 512, mode)
+    cache, _ = _cache(pg, d, q8, 341)
+    k8 = torch.zeros(pg.kv_rows, 128, dtype=torch.uint8, device="cuda")
+    ks = torch.zeros(pg.kv_rows, device="cuda")
+    k_new = torch.randn(pg.rows, 128, device="cuda")
+    q = _queries(pg.rows, d, 342)
+    idx = None if every else torch.from_numpy(ref.random_selection(pg, 512, 343)).cuda()
+    n = (dsa.dsa_sparse_mla_q8_workspace_size if q8 else dsa.dsa_sparse_mla_workspace_size)(
+        pb, pg.rows)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    append = dsa.dsa_cache_append_q8 if q8 else dsa.dsa_cache_append
+    attend = dsa.dsa_sparse_mla_fwd_q8 if q8 else dsa.dsa_sparse_mla_fwd
+    steps = 12
+    kv_new = [ref.latents(pg.rows, d, 350 + i) for i in range(steps)]
+    runs = []
+    for idle in (False, True):
+        outs = [(torch.empty(pg.rows, d["h"], d["d_v"], dtype=torch.bfloat16, device="cuda"),
+                 torch.empty(pg.rows, d["h"], device="cuda")) for _ in range(steps)]
+        torch.cuda.synchronize()
+        for x, (out, lse) in zip(kv_new, outs):
+            assert append(pb, k_new, x, k8, ks, cache) == dsa.DSA_OK
+            if idle:
+                torch.cuda.synchronize()
+            assert attend(pb, q, cache, idx, 0, pg.rows, out, lse, ws, n) == dsa.DSA_OK
+        torch.cuda.synchronize()
+        runs.append(outs)
+    for (o, l), (oi, li) in zip(*runs):
+        assert torch.equal(o, oi) and torch.equal(l, li)
+    assert not torch.equal(runs[0][0][0], runs[0][1][0])
