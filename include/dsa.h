@@ -65,8 +65,11 @@
  *            and the last of its seq_lens[b] cached tokens: row r has position pos =
  *            seq_lens[b] - (cu[b+1] - r) and sees keys 0..pos.  Keys lie where DECODE has them.
  *            A context above max_seqlen is taken as max_seqlen, and a row whose position comes
- *            out negative has no keys; both set DSA_DEVICE_BAD_INDEX.  The training calls take
- *            no chunks (DSA_ERR_INVALID_ARG).
+ *            out negative has no keys; both set DSA_DEVICE_BAD_INDEX.  seq_lens and block_table may
+ *            change between replays of a captured call.  cu_seqlens may not differ from its host
+ *            copy, which the launches are planned with, except that it may end earlier while the
+ *            sequences in front keep their rows: the rows behind it have no keys.  The training
+ *            calls take no chunks (DSA_ERR_INVALID_ARG).
  *   Key indices returned by dsa_topk and consumed by dsa_sparse_mla_fwd are LOGICAL
  *   positions within the sequence.
  */
@@ -139,7 +142,8 @@ typedef struct {
  *   k_idx   e4m3 [num_kv_rows, d_idx]            k_scale     fp32 [num_kv_rows]
  *   scores  fp32 [row_count, ld_scores]: scores[(t - row_begin) * ld + s] for s <= pos(t);
  *           entries past pos(t) are left untouched.  ld_scores >= max pos(t) + 1 over
- *           the rows and a multiple of 4.
+ *           the rows (DECODE, CHUNK, whose contexts the host does not know: >= max_seqlen) and a
+ *           multiple of 4.
  *   hist    optional uint32 [row_count, DSA_TOPK_HIST_BINS], zero on entry: the indexer ADDS
  *           to row t - row_begin the count of each written score in the bin of its first
  *           radix digit (the top 11 bits of the order-preserving key the selection sorts on),
@@ -207,7 +211,10 @@ DSA_API size_t dsa_sparse_mla_workspace_size_for(const dsa_dims_t* dims, const d
                                                  int32_t row_count, int32_t sm_count,
                                                  size_t max_bytes);
 
-/* Stage 3.  Sparse MLA-MQA forward for rows [row_begin, row_begin + row_count).
+/* Stage 3.  Sparse MLA-MQA forward for rows [row_begin, row_begin + row_count).  Single tokens over
+ * bf16 pages may be passed as DECODE or as CHUNK with one row a sequence: the same results within
+ * rounding, by different kernels (CHUNK takes some 0.6 of the time: 2048 keys each, 1 / 64 / 592
+ * tokens in 17 / 55 / 496 us, DECODE in 29 / 94 / 793).
  *   q    bf16 [total_rows, h, d_qk]   (indexed by absolute row)
  *   kv   bf16 [num_kv_rows, d_qk]
  *   idx  int32 [row_count, topk] logical key indices (-1 = unused), relative to row_begin,
@@ -265,15 +272,16 @@ DSA_API size_t dsa_forward_workspace_size_for(const dsa_dims_t* dims, const dsa_
  * the rows per chunk of sequence `seq` (the last chunk of a sequence may be shorter; with
  * idx_out NULL the first min(L, topk) rows run dense attention before the chunks start).  Each
  * chunk is one indexer, one top-k and one attention launch over its rows.  DECODE: the batch
- * (one chunk).  0 on invalid arguments. */
+ * (one chunk).  CHUNK: the rows per launch, over all sequences (`seq` is not used).  0 on invalid
+ * arguments. */
 DSA_API int32_t dsa_forward_chunk_rows_for(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
                                            int32_t seq, int32_t sm_count);
 
 /* The whole path for all seqs->total_rows query rows.  Inputs as for the three stages.
  *   idx_out  optional int32 [total_rows, topk]: the selected indices (NULL = not kept).
  *            When NULL, rows with at most topk prior keys (the first topk rows of each prefill
- *            sequence; a decode batch whose max_seqlen <= topk) skip the indexer and the top-k,
- *            whose selection would be all of their keys, and run dense attention.
+ *            sequence; a decode batch or a chunk problem whose max_seqlen <= topk) skip the indexer
+ *            and the top-k, whose selection would be all of their keys, and run dense attention.
  *   sel_out  optional fp32 [total_rows, topk]: the indexer score of each selected key, as
  *            dsa_topk writes it (requires idx_out; else DSA_ERR_INVALID_ARG).
  *   out, lse as for dsa_sparse_mla_fwd. */
@@ -308,8 +316,8 @@ DSA_API dsa_status_t dsa_forward_rows(const dsa_dims_t* dims, const dsa_seqs_t* 
  * selection -> sparse core attention", "DeepSeek V3.2-Exp Cuts Long-Context Costs with DeepSeek
  * Sparse Attention (DSA)", pipeline summary: the indexer reads keys in FP8).  DECODE or CHUNK
  * mode (CHUNK: total_rows new tokens, row r at its own position, skipped and reported when its
- * context is above max_seqlen).  For each sequence b of a DECODE call the new token sits at position p = seq_lens[b] - 1 (the lengths already
- * count it); it is written at physical row block_table[b][p / block_size] * block_size +
+ * context is above max_seqlen).  For each sequence b of a DECODE call the new token sits at
+ * position p = seq_lens[b] - 1 (the lengths already count it); it is written at physical row block_table[b][p / block_size] * block_size +
  * p % block_size, or b * max_seqlen + p when block_table is NULL:
  *   k_new     fp32 [batch, d_idx]: the new token's indexer key, quantised per token: scale =
  *             amax / 448 in fp32 (1 when amax = 0), codes = the e4m3 value nearest to x / scale
@@ -319,8 +327,8 @@ DSA_API dsa_status_t dsa_forward_rows(const dsa_dims_t* dims, const dsa_seqs_t* 
  *   kv_new    bf16 [batch, d_qk]: the new token's latent row, copied unchanged
  *   k_cache   e4m3 [num_kv_rows, d_idx], k_scale_cache fp32 [num_kv_rows], kv_cache bf16
  *             [num_kv_rows, d_qk]: caller-owned caches, written at the one row per sequence
- * All pointers 16-byte aligned.  An entry whose position or block falls outside the caches is
- * skipped and sets DSA_DEVICE_BAD_INDEX in *dev_status. */
+ * All pointers 16-byte aligned.  An entry whose position falls outside the caches, or whose block is
+ * not wholly inside them, is skipped and sets DSA_DEVICE_BAD_INDEX in *dev_status. */
 DSA_API dsa_status_t dsa_cache_append(const dsa_dims_t* dims, const dsa_seqs_t* seqs,
                                       const float* k_new, const uint16_t* kv_new,
                                       uint8_t* k_cache, float* k_scale_cache, uint16_t* kv_cache,
@@ -335,9 +343,11 @@ DSA_API dsa_status_t dsa_cache_append(const dsa_dims_t* dims, const dsa_seqs_t* 
  *   2 (d_qk - d_v)   the rotary dims in bf16, unquantised
  * A scale is the smallest power of two s with max|x| <= 448 s over its 128 values (1 when all are
  * 0; its exponent kept within [-100, 119]), a code the e4m3 value nearest to x / s (ties to even,
- * saturating), so that |x - s code| <= 2^-4 |x| + 2^-10 s.  s code is exact in bf16: reading back
- * and attending round nothing more.  128 values that hold an infinity or a NaN get a NaN scale
- * and read back as NaN.  Row number r of the cache starts at byte r * dsa_q8_row_bytes; rows,
+ * saturating), so that |x - s code| <= 2^-4 |x| + 2^-10 s for |x| <= 448 * 2^119; the finite bf16
+ * values above that become +-448 * 2^119.  s code is exact in bf16: reading back and attending
+ * round nothing more.  128 values that hold an infinity or a NaN get a NaN scale and read back as
+ * NaN.  The library writes no NaN code; in a cache filled elsewhere 0x7F and 0xFF must not occur
+ * (they would count as +-480 s).  Row number r of the cache starts at byte r * dsa_q8_row_bytes; rows,
  * pages and block tables are those of the bf16 cache. */
 
 /* Bytes of one 8-bit latent row; 0 when (d_qk, d_v) is not a supported pair. */

@@ -563,11 +563,11 @@ size_t mla_ws_bytes(const dsa_dims_t& d, int splits, int32_t row_count) {
 }
 
 // Split-KV slices per row of the paged attention: the smallest estimated time in units of a tile
-// (1.1 us).  A CTA pair costs its tiles and some 10 more (indices, Q, filling and draining the
-// pipeline, output), combining costs 2 and 0.05 a row and split (its traffic).  Measured at
-// 2048 keys over 8-bit rows: 1 row, 4 / 8 / 16 splits: 23.7 / 19.5 / 18.0 us; 16 rows, 1 / 2 / 4:
-// 50.0 / 35.9 / 27.0; 32 rows, 1 / 2: 52.0 / 42.4; 80 rows, 1 / 2: 123 / 125; 100 rows, 1 / 2:
-// 127 / 132.
+// (1.1 us).  A CTA pair costs its tiles and some 10 more (launch, indices, Q, filling and draining
+// the pipeline, output), combining costs 2 and 0.05 a row and split (its traffic).  Measured at
+// 2048 keys over 8-bit rows: 1 row, 4 / 8 / 11 / 16 splits: 21.2 / 17.3 / 16.7 / 16.0 us; 16 rows,
+// 1 / 2 / 4: 49.0 / 33.9 / 25.1; 32 rows, 1 / 2: 50.4 / 38.5; 64 rows, 1 / 2: 58.2 / 79.9; 80 rows,
+// 1 / 2: 112 / 115; 100 rows, 1 / 2: 113 / 119.
 int paged_splits(const dsa_dims_t& d, const dsa_seqs_t& s, int32_t row_count, int sm_count,
                  size_t max_ws = SIZE_MAX) {
   if (s.mode == DSA_PREFILL || row_count <= 0) return 1;

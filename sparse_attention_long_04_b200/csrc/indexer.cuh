@@ -23,8 +23,9 @@
 // later tiles.  Decode (one query row, N = 64) runs two epilogue warpgroups on alternate tiles;
 // prefill and chunks (N = 256) split each tile's columns over four warpgroups, one query row each:
 // 512 rows x 65536 keys in 412 us, 1650 cycles a tile, of which the MMAs take 512.  The epilogue
-// bounds it: 64 maxima and 32 packed FMAs a thread and tile are 740 cycles of a scheduler's time
-// over its four warps (maxima 2 cycles, packed FMAs 3), the waits and loads around them the rest.
+// bounds it: 64 maxima and 32 packed FMAs a thread and tile take a scheduler and its four warps 740
+// cycles (measured alone: the maxima 530, the FMAs 385, on pipes that overlap in part), the waits
+// and loads around them the rest.
 //
 // Fused first digit of the top-k (when `hist` is given): as it writes a score, each epilogue
 // thread also counts it in its query row's histogram of the top 11 bits of the order-preserving

@@ -16,14 +16,15 @@
 // to its partner, counted in bytes on the receiver's barriers.
 //
 // Both CTAs gathering whole keys and computing all logits instead (nothing exchanged): 592 rows x
-// 2048 keys of (576, 512) take 408 us from the bf16 cache and 496 us from the 8-bit one, against 349
+// 2048 keys of (576, 512) take 408 us from the bf16 cache and 496 us from the 8-bit one, against 362
 // and 398 here.  There the shared-memory pipe is the limit (bf16 rows 98% busy: 36 KB of copies in
 // and 64 + 72 KB of MMA operands a tile out).  Here no pipe is above 56%: a tile takes some 2050
 // cycles because a softmax warp's chain of waits, from a tile's product to its probabilities, is
 // 3500-4000 with two warps a quarter in turn, and 15% of a CTA's time is its fixed cost (indices, Q,
 // filling, draining, output).  Sending the logits by bulk copies, a second logit buffer, the QK
 // issuer freed of the rescaling: each as slow or slower (398 -> 411, 404, 391 with 5 slots but
-// bf16 349 -> 382).
+// bf16 349 -> 382; measured before the fence of mbar_arrive_cluster_read, which cost bf16 rows the
+// 3% between 349 and 362).
 //
 // Tensor work of a tile at (576, 512): 16 or 20 QK MMAs of N = 64 (32 cycles each, A in TMEM) and
 // 4 PV MMAs of N = 256 (128 cycles): 1090 cycles on average.  The MMAs are issued by one elected
@@ -923,8 +924,8 @@ __global__ void __launch_bounds__(512, 1)
 
 // Merge the splits' partials by their LSE: O = sum_i e^(LSE_i - LSE) O_i, LSE = log sum e^LSE_i.
 // One CTA per (row, head); a NaN partial makes the head NaN.  Launched while the attention kernel
-// runs, and every load is on its way before the first is used: one token over 2048 keys in 8
-// splits takes 19.5 us with the attention, 21.5 with a plain launch and the loads in loops.
+// runs, and every load is on its way before the first is used: one token over 2048 keys in 16
+// splits takes 16.0 us with the attention, 17.6 with a plain launch.
 template <int D_V, int MAX_SPLITS>
 __global__ void __launch_bounds__(D_V / 4) dsa_paged_combine_kernel(const PagedMlaParams p) {
   wait_prior_grid();
